@@ -126,6 +126,18 @@ typedef enum {
 
 typedef enum { KRONQ_F32 = 0, KRONQ_BF16 = 1 } kronq_dtype;
 
+/* Activations of the dense operators (kronq_linear, kronq_gated):
+ *   SILU z / (1 + e^-z);  GELU z (1 + erf(z / sqrt 2)) / 2;
+ *   GELU_TANH z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2.
+ * The derivative of RELU at 0 is 0. */
+typedef enum {
+  KRONQ_ACT_NONE = 0,
+  KRONQ_ACT_RELU = 1,
+  KRONQ_ACT_SILU = 2,
+  KRONQ_ACT_GELU = 3,
+  KRONQ_ACT_GELU_TANH = 4
+} kronq_act;
+
 /* Factorisation of one side's dimension d = had * m (see the spec above). */
 typedef struct {
   int64_t had; /* power of two, >= 1 */
@@ -385,6 +397,144 @@ kronq_status kronq_dequant_matvec(kronq_stream_t stream, const kronq_opts *opts,
                                   const float *scales, const uint8_t *zeros, int64_t d_out,
                                   int64_t d_in, const float *x, int64_t n_tokens, float *y,
                                   void *ws, size_t ws_bytes, int32_t *info_dev);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The operators of a calibration pass. H_X and H_G need a sublayer's inputs X
+ * and the gradients G of its outputs from one backward pass [gptget-en
+ * Methodology; wmrh §二]; the pages name no routine that makes them. The calls
+ * below are that pass for a feed-forward block: kronq_gated (gate and up),
+ * kronq_linear (down with the residual stream, any plain sublayer, the head),
+ * kronq_distill_* (the loss of the model's answers against a teacher's top
+ * logits, and its gradient), and the backward calls, whose dZ, Gg and Gu are
+ * the sublayers' G.
+ *
+ * Conventions of this section, besides those at the top:
+ *   - Matrices marked bf16 are __nv_bfloat16, row-major with a row stride
+ *     (ld..., in elements) that is a multiple of 8 and at least the width,
+ *     16-byte aligned; widths and row counts are arbitrary (a stride that is
+ *     not a multiple of 8 or a misaligned matrix: UNSUPPORTED). Elements
+ *     between the width and the stride are neither read into a result nor
+ *     written. Products accumulate in fp32; every output is rounded once.
+ *   - *info_dev is NOT cleared: it is written only on failure (the first
+ *     failure stays), so that one word, cleared once by the caller, serves a
+ *     whole pass. TIMEOUT when a pipeline wait ran out (the outputs are then
+ *     not valid).
+ *   - Outputs may not overlap inputs or one another, except where the call
+ *     says so. No workspace is needed, and results do not depend on how the
+ *     work was split: the same call gives the same bits.
+ *   - n = 0 (no tokens) is allowed: weight and bias gradients are then 0.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Y = act(X W^T + bias) + R.
+ * X: n x d_in bf16, W: d_out x d_in bf16, bias: d_out fp32 or NULL, R: n x
+ * d_out bf16 or NULL (may be Y itself, with the same stride), Y: n x d_out
+ * bf16. Z: NULL, or n x d_out bf16, which receives the pre-activations
+ * X W^T + bias that kronq_linear_bwd takes.
+ */
+kronq_status kronq_linear(kronq_stream_t stream, const void *X, int64_t n,
+                          int64_t d_in, int64_t ldx, const void *W,
+                          int64_t d_out, int64_t ldw, const float *bias,
+                          kronq_act act, void *Z, int64_t ldz, const void *R,
+                          int64_t ldr, void *Y, int64_t ldy, int32_t *info_dev);
+
+/*
+ * Backward pass of kronq_linear (the gradient of R is dY itself):
+ *   dZ = dY * act'(Z)        n x d_out bf16: the sublayer's G
+ *   db = sum over rows of dZ (before its rounding), fp32 d_out, or NULL
+ *   dX = dZ W + dXr          n x d_in bf16, or NULL; dXr: bf16 addend or NULL
+ *                            (a residual stream's gradient; may be dX itself)
+ *   dW = dZ^T X              d_out x d_in bf16, or NULL
+ * The products take dZ as rounded to bf16. With KRONQ_ACT_NONE dZ = dY: Z is
+ * not read, and dZ may be NULL or dY (otherwise it receives a copy). dZ may
+ * also be dY or Z with another activation (the same stride). X may be NULL
+ * without dW, W without dX.
+ */
+kronq_status kronq_linear_bwd(kronq_stream_t stream, const void *dY,
+                              int64_t lddy, const void *Z, int64_t ldz,
+                              kronq_act act, const void *X, int64_t ldx,
+                              const void *W, int64_t ldw, int64_t n,
+                              int64_t d_in, int64_t d_out, void *dZ,
+                              int64_t lddz, float *db, const void *dXr,
+                              int64_t lddxr, void *dX, int64_t lddx, void *dW,
+                              int64_t lddw, int32_t *info_dev);
+
+/*
+ * The gated pair of a feed-forward block: A = X Wg^T, U = X Wu^T,
+ * H = act(A) * U (H is the down projection's X).
+ * X: n x d bf16; Wg, Wu: f x d bf16, both with stride ldw; H: n x f bf16.
+ * A, U: both NULL, or both n x f bf16 with stride ldau, kept for
+ * kronq_gated_bwd.
+ */
+kronq_status kronq_gated(kronq_stream_t stream, const void *X, int64_t n,
+                         int64_t d, int64_t ldx, const void *Wg, const void *Wu,
+                         int64_t f, int64_t ldw, kronq_act act, void *A,
+                         void *U, int64_t ldau, void *H, int64_t ldh,
+                         int32_t *info_dev);
+
+/*
+ * Backward pass of kronq_gated, from dH (n x f bf16) and the kept A, U:
+ *   Gg = dH * U * act'(A),  Gu = dH * act(A)   n x f bf16, stride ldg: the
+ *                           G of the gate and the up sublayer
+ *   dX = Gg Wg + Gu Wu + dXr  n x d bf16, or NULL; dXr: bf16 addend or NULL
+ *                           (may be dX itself)
+ *   dWg = Gg^T X, dWu = Gu^T X  f x d bf16 with stride lddw, both or neither
+ * The products take Gg and Gu as rounded to bf16. Gg or Gu may be A, U or dH
+ * (the same stride; not both the same matrix). X may be NULL without the
+ * weight gradients, Wg and Wu without dX.
+ */
+kronq_status kronq_gated_bwd(kronq_stream_t stream, const void *dH,
+                             int64_t lddh, const void *A, const void *U,
+                             int64_t ldau, kronq_act act, const void *X,
+                             int64_t ldx, const void *Wg, const void *Wu,
+                             int64_t ldw, int64_t n, int64_t d, int64_t f,
+                             void *Gg, void *Gu, int64_t ldg, const void *dXr,
+                             int64_t lddxr, void *dX, int64_t lddx, void *dWg,
+                             void *dWu, int64_t lddw, int32_t *info_dev);
+
+/*
+ * Distillation from a teacher's top logits. Z: n x vocab student logits
+ * (zdtype, any stride ldz >= vocab). A row keeps up to k teacher logits
+ * T (n x k, tdtype) at the vocabulary places idx (n x k int32; T and idx
+ * share the stride ldt): entries with idx < 0 are padding, and entries with
+ * idx >= vocab are left out and reported as INVALID_ARG in *info_dev.
+ *   p = softmax(T / tau) over the row's kept entries
+ *   lse = log sum_v exp(Z_v / tau),  log q_v = Z_v / tau - lse
+ *   loss = tau^2 sum_j p_j (log p_j - log q_{idx_j})    (p_j = 0 adds 0)
+ *   dZ_v = weight tau (q_v - sum over {j: idx_j = v} of p_j)
+ * so dZ is the gradient of sum over rows of weight * loss. A place may be
+ * named more than once: its p's add up. weight: n fp32, or NULL for all 1. A
+ * row of weight 0, or one that keeps no entry, does not count: its logits are
+ * not read, and its loss, lse and gradient are 0. Row sums are fp32, the
+ * row's logarithms and its loss fp64, rounded once. info_dev: NONFINITE when
+ * the loss of a row that counts is not finite.
+ * _fwd writes loss and lse (n fp32), _bwd takes that lse and writes dZ (n x
+ * vocab, zdtype), _step does both while a row is on the chip. dZ may be Z
+ * (the same stride). 1 <= k <= 1024, 1e-4 <= tau <= 1e4, vocab < 2^31;
+ * pointers aligned to their element. A row whose logits are all -inf, or that
+ * holds a NaN or +inf, has lse and gradient NaN.
+ */
+kronq_status kronq_distill_fwd(kronq_stream_t stream, const void *Z,
+                               kronq_dtype zdtype, int64_t n, int64_t vocab,
+                               int64_t ldz, const void *T, kronq_dtype tdtype,
+                               const int32_t *idx, int64_t k, int64_t ldt,
+                               float tau, const float *weight, float *loss,
+                               float *lse, int32_t *info_dev);
+kronq_status kronq_distill_bwd(kronq_stream_t stream, const void *Z,
+                               kronq_dtype zdtype, int64_t n, int64_t vocab,
+                               int64_t ldz, const void *T, kronq_dtype tdtype,
+                               const int32_t *idx, int64_t k, int64_t ldt,
+                               float tau, const float *weight, const float *lse,
+                               void *dZ, int64_t lddz, int32_t *info_dev);
+kronq_status kronq_distill_step(kronq_stream_t stream, const void *Z,
+                                kronq_dtype zdtype, int64_t n, int64_t vocab,
+                                int64_t ldz, const void *T, kronq_dtype tdtype,
+                                const int32_t *idx, int64_t k, int64_t ldt,
+                                float tau, const float *weight, float *loss,
+                                float *lse, void *dZ, int64_t lddz,
+                                int32_t *info_dev);
 
 /* Workspace bytes needed by one call (opts may be NULL except for BIIP and
  * QUANT). Returns 0 for unsupported arguments. */

@@ -1,0 +1,58 @@
+// The activations of the dense operators and their derivatives, in fp32.
+//   silu       z s(z),                s(z) = 1 / (1 + exp(-z))
+//   gelu       z P(z),                P(z) = erfc(-z / sqrt 2) / 2
+//   gelu_tanh  z s(2 v),              v = sqrt(2 / pi) (z + 0.044715 z^3):
+//              (1 + tanh v) / 2 = s(2 v), which keeps its relative accuracy
+//              where tanh v is close to -1
+// erfc in place of 1 + erf for the same reason. A NaN stays a NaN.
+#pragma once
+
+#include "common.cuh"
+
+namespace kronq {
+
+__device__ __forceinline__ float logistic(float z) {
+  return __fdividef(1.f, 1.f + __expf(-z));
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_f(float z) {
+  if constexpr (ACT == KRONQ_ACT_RELU) return z < 0.f ? 0.f : z;
+  if constexpr (ACT == KRONQ_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+  if constexpr (ACT == KRONQ_ACT_GELU) return 0.5f * z * erfcf(-0.70710678f * z);
+  if constexpr (ACT == KRONQ_ACT_GELU_TANH) {
+    const float v2 = 1.5957691216f * fmaf(0.044715f * z * z, z, z);
+    return __fdividef(z, 1.f + __expf(-v2));
+  }
+  return z;
+}
+
+// value and derivative
+template <int ACT>
+__device__ __forceinline__ void act_df(float z, float &h, float &dh) {
+  if constexpr (ACT == KRONQ_ACT_RELU) {
+    h = z < 0.f ? 0.f : z;
+    dh = z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);   // NaN stays
+  } else if constexpr (ACT == KRONQ_ACT_SILU) {
+    const float s = logistic(z);
+    h = z * s;
+    dh = fmaf(h, 1.f - s, s);
+  } else if constexpr (ACT == KRONQ_ACT_GELU) {
+    const float c = 0.5f * erfcf(-0.70710678f * z);
+    h = z * c;
+    dh = fmaf(z * 0.39894228f, __expf(-0.5f * z * z), c);
+  } else if constexpr (ACT == KRONQ_ACT_GELU_TANH) {
+    // beyond |z| = 30 the derivative's second term is 0 in fp32; the clamp
+    // keeps its polynomial finite there
+    const float zc = fminf(fmaxf(z, -30.f), 30.f);
+    const float s = logistic(1.5957691216f * fmaf(0.044715f * zc * zc, z, z));
+    const float dv2 = 1.5957691216f * fmaf(3.f * 0.044715f * zc, zc, 1.f);
+    h = z * s;
+    dh = fmaf(h * (1.f - s), dv2, s);
+  } else {
+    h = z;
+    dh = 1.f;
+  }
+}
+
+}  // namespace kronq

@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <numeric>
 #include <vector>
 
@@ -20,6 +21,112 @@ bool rot_ok(const kronq_rot &r, int64_t d) {
 
 bool aligned(const void *p, size_t a) {
   return reinterpret_cast<uintptr_t>(p) % a == 0;
+}
+
+// ---- matrices of the dense operators
+constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxWidth = int64_t(1) << 24;
+
+struct View {
+  const void *p;
+  int64_t ld, rows, cols;
+  int es;  // bytes per element
+};
+
+// Whether two strided matrices share an element's bytes. With equal strides
+// the test is exact (column slices of one wide matrix do not overlap);
+// otherwise it compares their address ranges.
+bool overlap(const View &a, const View &b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.cols <= 0 || b.cols <= 0) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  if (pb < pa) return overlap(b, a);
+  const uint64_t la = uint64_t(a.ld) * a.es, lb = uint64_t(b.ld) * b.es;
+  const uint64_t ca = uint64_t(a.cols) * a.es, cb = uint64_t(b.cols) * b.es;
+  const uint64_t off = pb - pa;
+  if (off >= (uint64_t(a.rows) - 1) * la + ca) return false;
+  if (la != lb) return true;
+  const uint64_t r = off / la, c = off % la;  // b starts in a's row r at byte c
+  return (c < ca && r < uint64_t(a.rows)) || (c + cb > la && r + 1 < uint64_t(a.rows));
+}
+bool same(const View &a, const View &b) { return a.p == b.p && a.ld == b.ld && a.es == b.es; }
+// a may be exactly b, but may not overlap it in another way
+bool bad_alias(const View &a, const View &b) { return !same(a, b) && overlap(a, b); }
+
+View bf16_view(const void *p, int64_t rows, int64_t cols, int64_t ld) {
+  return View{p, ld, rows, cols, 2};
+}
+
+// The layout rules of a bf16 matrix (absent ones pass).
+kronq_status check_views(std::initializer_list<View> vs) {
+  for (const View &v : vs)
+    if (v.p && v.ld < v.cols) return KRONQ_ERR_INVALID_ARG;
+  for (const View &v : vs)
+    if (v.p && (v.ld % 8 || !aligned(v.p, 16))) return KRONQ_ERR_UNSUPPORTED;
+  return KRONQ_OK;
+}
+
+// No output overlaps an input or another output.
+bool any_overlap(std::initializer_list<View> outs, std::initializer_list<View> ins) {
+  for (const View *o = outs.begin(); o != outs.end(); ++o) {
+    for (const View &i : ins)
+      if (overlap(*o, i)) return true;
+    for (const View *q = o + 1; q != outs.end(); ++q)
+      if (overlap(*o, *q)) return true;
+  }
+  return false;
+}
+
+bool act_ok(int a) { return a >= KRONQ_ACT_NONE && a <= KRONQ_ACT_GELU_TANH; }
+
+Mat mat(const View &v) { return Mat{const_cast<void *>(v.p), v.ld}; }
+
+kronq_status run_distill(kronq_stream_t stream, const void *Z, kronq_dtype zdtype, int64_t n,
+                         int64_t vocab, int64_t ldz, const void *T, kronq_dtype tdtype,
+                         const int32_t *idx, int64_t k, int64_t ldt, float tau,
+                         const float *weight, float *loss, float *lse, void *dZ, int64_t lddz,
+                         int32_t *info_dev) {
+  if (n < 0 || vocab <= 0 || k <= 0 || ldz < vocab || ldt < k || !info_dev ||
+      (dZ && lddz < vocab))
+    return KRONQ_ERR_INVALID_ARG;
+  if ((zdtype != KRONQ_F32 && zdtype != KRONQ_BF16) ||
+      (tdtype != KRONQ_F32 && tdtype != KRONQ_BF16))
+    return KRONQ_ERR_INVALID_ARG;
+  if (!(tau >= 1e-4f && tau <= 1e4f)) return KRONQ_ERR_INVALID_ARG;
+  if (n > 0 && (!Z || !T || !idx)) return KRONQ_ERR_INVALID_ARG;
+  const int ez = zdtype == KRONQ_BF16 ? 2 : 4, et = tdtype == KRONQ_BF16 ? 2 : 4;
+  if (!aligned(Z, ez) || !aligned(dZ, ez) || !aligned(T, et) || !aligned(idx, 4) ||
+      !aligned(weight, 4) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(info_dev, 4))
+    return KRONQ_ERR_INVALID_ARG;
+  if (bad_alias(View{dZ, lddz, n, vocab, ez}, View{Z, ldz, n, vocab, ez}))
+    return KRONQ_ERR_INVALID_ARG;
+  if (any_overlap({View{dZ, lddz, n, vocab, ez}, View{loss, n, 1, n, 4},
+                   View{loss ? lse : nullptr, n, 1, n, 4}},
+                  {View{T, ldt, n, k, et}, View{idx, ldt, n, k, 4}, View{weight, n, 1, n, 4},
+                   View{loss ? nullptr : lse, n, 1, n, 4}}))
+    return KRONQ_ERR_INVALID_ARG;
+  if (any_overlap({View{loss, n, 1, n, 4}, View{loss ? lse : nullptr, n, 1, n, 4}},
+                  {View{Z, ldz, n, vocab, ez}}))
+    return KRONQ_ERR_INVALID_ARG;
+  if (vocab > 0x7fffffff || n > 0x7fffffff || k > 1024) return KRONQ_ERR_UNSUPPORTED;
+  KQ_TRY(require_sm100());
+  DistillArgs a;
+  a.Z = Z;
+  a.z_bf16 = zdtype == KRONQ_BF16;
+  a.n = n;
+  a.vocab = vocab;
+  a.ldz = ldz;
+  a.T = T;
+  a.t_bf16 = tdtype == KRONQ_BF16;
+  a.idx = idx;
+  a.k = static_cast<int>(k);
+  a.ldt = ldt;
+  a.tau = tau;
+  a.weight = weight;
+  a.loss = loss;
+  a.lse = lse;
+  a.dZ = dZ;
+  a.lddz = lddz;
+  a.info = info_dev;
+  return distill(as_stream(stream), a);
 }
 
 }  // namespace
@@ -348,6 +455,132 @@ kronq_status kronq_allocate_bits(const double *score, const int64_t *numel,
     }
   }
   return KRONQ_OK;
+}
+
+kronq_status kronq_linear(kronq_stream_t stream, const void *X, int64_t n, int64_t d_in,
+                          int64_t ldx, const void *W, int64_t d_out, int64_t ldw,
+                          const float *bias, kronq_act act, void *Z, int64_t ldz, const void *R,
+                          int64_t ldr, void *Y, int64_t ldy, int32_t *info_dev) {
+  if (n < 0 || d_in <= 0 || d_out <= 0 || !act_ok(act) || !info_dev || !W ||
+      (n > 0 && (!X || !Y)) || !aligned(bias, 4) || !aligned(info_dev, 4))
+    return KRONQ_ERR_INVALID_ARG;
+  const View x = bf16_view(X, n, d_in, ldx), w = bf16_view(W, d_out, d_in, ldw),
+             z = bf16_view(Z, n, d_out, ldz), r = bf16_view(R, n, d_out, ldr),
+             y = bf16_view(Y, n, d_out, ldy), b = View{bias, d_out, 1, d_out, 4};
+  KQ_TRY(check_views({x, w, z, r, y}));
+  if (any_overlap({y, z}, {x, w, b}) || bad_alias(y, r) || overlap(z, r))
+    return KRONQ_ERR_INVALID_ARG;
+  if (n > kMaxRows || d_in > kMaxWidth || d_out > kMaxWidth) return KRONQ_ERR_UNSUPPORTED;
+  if (n == 0) return KRONQ_OK;
+  KQ_TRY(require_sm100());
+  return linear_fwd(as_stream(stream), n, d_in, d_out, mat(x), mat(w), bias, act, mat(z), mat(r),
+                    mat(y), info_dev);
+}
+
+kronq_status kronq_linear_bwd(kronq_stream_t stream, const void *dY, int64_t lddy, const void *Z,
+                              int64_t ldz, kronq_act act, const void *X, int64_t ldx,
+                              const void *W, int64_t ldw, int64_t n, int64_t d_in, int64_t d_out,
+                              void *dZ, int64_t lddz, float *db, const void *dXr, int64_t lddxr,
+                              void *dX, int64_t lddx, void *dW, int64_t lddw,
+                              int32_t *info_dev) {
+  if (n < 0 || d_in <= 0 || d_out <= 0 || !act_ok(act) || !info_dev || !aligned(db, 4) ||
+      !aligned(info_dev, 4) || (n > 0 && !dY) ||
+      (n > 0 && act != KRONQ_ACT_NONE && (!Z || !dZ)) || (n > 0 && dW && !X) ||
+      (n > 0 && dX && !W) || (dXr && !dX))
+    return KRONQ_ERR_INVALID_ARG;
+  const View dy = bf16_view(dY, n, d_out, lddy),
+             z = bf16_view(act == KRONQ_ACT_NONE ? nullptr : Z, n, d_out, ldz),
+             x = bf16_view(dW ? X : nullptr, n, d_in, ldx),
+             w = bf16_view(dX ? W : nullptr, d_out, d_in, ldw), dz = bf16_view(dZ, n, d_out, lddz),
+             dxr = bf16_view(dXr, n, d_in, lddxr), dx = bf16_view(dX, n, d_in, lddx),
+             dw = bf16_view(dW, d_out, d_in, lddw), b = View{db, d_out, 1, d_out, 4};
+  KQ_TRY(check_views({dy, z, x, w, dz, dxr, dx, dw}));
+  if (bad_alias(dz, dy) || bad_alias(dz, z) || bad_alias(dx, dxr) ||
+      any_overlap({dz, dx, dw, b}, {x, w}) || any_overlap({dx, dw, b}, {dy, z}) ||
+      any_overlap({dz, dw, b}, {dxr}))
+    return KRONQ_ERR_INVALID_ARG;
+  if (n > kMaxRows || d_in > kMaxWidth || d_out > kMaxWidth) return KRONQ_ERR_UNSUPPORTED;
+  KQ_TRY(require_sm100());
+  return linear_bwd(as_stream(stream), n, d_in, d_out, mat(dy), mat(z), act, mat(x), mat(w),
+                    mat(dz), db, mat(dxr), mat(dx), mat(dw), info_dev);
+}
+
+kronq_status kronq_gated(kronq_stream_t stream, const void *X, int64_t n, int64_t d, int64_t ldx,
+                         const void *Wg, const void *Wu, int64_t f, int64_t ldw, kronq_act act,
+                         void *A, void *U, int64_t ldau, void *H, int64_t ldh,
+                         int32_t *info_dev) {
+  if (n < 0 || d <= 0 || f <= 0 || !act_ok(act) || !info_dev || !Wg || !Wu ||
+      (n > 0 && (!X || !H)) || (A == nullptr) != (U == nullptr) || !aligned(info_dev, 4))
+    return KRONQ_ERR_INVALID_ARG;
+  const View x = bf16_view(X, n, d, ldx), wg = bf16_view(Wg, f, d, ldw),
+             wu = bf16_view(Wu, f, d, ldw), a = bf16_view(A, n, f, ldau),
+             u = bf16_view(U, n, f, ldau), h = bf16_view(H, n, f, ldh);
+  KQ_TRY(check_views({x, wg, wu, a, u, h}));
+  if (any_overlap({a, u, h}, {x, wg, wu})) return KRONQ_ERR_INVALID_ARG;
+  if (n > kMaxRows || d > kMaxWidth || f > kMaxWidth) return KRONQ_ERR_UNSUPPORTED;
+  if (n == 0) return KRONQ_OK;
+  KQ_TRY(require_sm100());
+  return gated_fwd(as_stream(stream), n, d, f, mat(x), mat(wg), mat(wu), act, mat(a), mat(u),
+                   mat(h), info_dev);
+}
+
+kronq_status kronq_gated_bwd(kronq_stream_t stream, const void *dH, int64_t lddh, const void *A,
+                             const void *U, int64_t ldau, kronq_act act, const void *X,
+                             int64_t ldx, const void *Wg, const void *Wu, int64_t ldw, int64_t n,
+                             int64_t d, int64_t f, void *Gg, void *Gu, int64_t ldg,
+                             const void *dXr, int64_t lddxr, void *dX, int64_t lddx, void *dWg,
+                             void *dWu, int64_t lddw, int32_t *info_dev) {
+  if (n < 0 || d <= 0 || f <= 0 || !act_ok(act) || !info_dev || !aligned(info_dev, 4) ||
+      (n > 0 && (!dH || !A || !U || !Gg || !Gu)) || (dWg == nullptr) != (dWu == nullptr) ||
+      (n > 0 && dWg && !X) || (n > 0 && dX && (!Wg || !Wu)) || (dXr && !dX))
+    return KRONQ_ERR_INVALID_ARG;
+  const View dh = bf16_view(dH, n, f, lddh), a = bf16_view(A, n, f, ldau),
+             u = bf16_view(U, n, f, ldau), x = bf16_view(dWg ? X : nullptr, n, d, ldx),
+             wg = bf16_view(dX ? Wg : nullptr, f, d, ldw),
+             wu = bf16_view(dX ? Wu : nullptr, f, d, ldw), gg = bf16_view(Gg, n, f, ldg),
+             gu = bf16_view(Gu, n, f, ldg), dxr = bf16_view(dXr, n, d, lddxr),
+             dx = bf16_view(dX, n, d, lddx), dwg = bf16_view(dWg, f, d, lddw),
+             dwu = bf16_view(dWu, f, d, lddw);
+  KQ_TRY(check_views({dh, a, u, x, wg, wu, gg, gu, dxr, dx, dwg, dwu}));
+  for (const View &g : {gg, gu})
+    if (bad_alias(g, dh) || bad_alias(g, a) || bad_alias(g, u)) return KRONQ_ERR_INVALID_ARG;
+  if (bad_alias(dx, dxr) || any_overlap({gg, gu, dx, dwg, dwu}, {x, wg, wu}) ||
+      any_overlap({dx, dwg, dwu}, {dh, a, u}) || any_overlap({gg, gu, dwg, dwu}, {dxr}))
+    return KRONQ_ERR_INVALID_ARG;
+  if (n > kMaxRows || d > kMaxWidth || f > kMaxWidth) return KRONQ_ERR_UNSUPPORTED;
+  KQ_TRY(require_sm100());
+  return gated_bwd(as_stream(stream), n, d, f, mat(dh), mat(a), mat(u), act, mat(x), mat(wg),
+                   mat(wu), mat(gg), mat(gu), mat(dxr), mat(dx), mat(dwg), mat(dwu), info_dev);
+}
+
+kronq_status kronq_distill_fwd(kronq_stream_t stream, const void *Z, kronq_dtype zdtype,
+                               int64_t n, int64_t vocab, int64_t ldz, const void *T,
+                               kronq_dtype tdtype, const int32_t *idx, int64_t k, int64_t ldt,
+                               float tau, const float *weight, float *loss, float *lse,
+                               int32_t *info_dev) {
+  if (n > 0 && (!loss || !lse)) return KRONQ_ERR_INVALID_ARG;
+  return run_distill(stream, Z, zdtype, n, vocab, ldz, T, tdtype, idx, k, ldt, tau, weight, loss,
+                     lse, nullptr, vocab, info_dev);
+}
+
+kronq_status kronq_distill_bwd(kronq_stream_t stream, const void *Z, kronq_dtype zdtype,
+                               int64_t n, int64_t vocab, int64_t ldz, const void *T,
+                               kronq_dtype tdtype, const int32_t *idx, int64_t k, int64_t ldt,
+                               float tau, const float *weight, const float *lse, void *dZ,
+                               int64_t lddz, int32_t *info_dev) {
+  if (n > 0 && (!lse || !dZ)) return KRONQ_ERR_INVALID_ARG;
+  return run_distill(stream, Z, zdtype, n, vocab, ldz, T, tdtype, idx, k, ldt, tau, weight,
+                     nullptr, const_cast<float *>(lse), dZ, lddz, info_dev);
+}
+
+kronq_status kronq_distill_step(kronq_stream_t stream, const void *Z, kronq_dtype zdtype,
+                                int64_t n, int64_t vocab, int64_t ldz, const void *T,
+                                kronq_dtype tdtype, const int32_t *idx, int64_t k, int64_t ldt,
+                                float tau, const float *weight, float *loss, float *lse, void *dZ,
+                                int64_t lddz, int32_t *info_dev) {
+  if (n > 0 && (!loss || !dZ)) return KRONQ_ERR_INVALID_ARG;
+  return run_distill(stream, Z, zdtype, n, vocab, ldz, T, tdtype, idx, k, ldt, tau, weight, loss,
+                     lse, dZ, lddz, info_dev);
 }
 
 uint64_t kronq_kernel_launches(void) { return launches(); }

@@ -124,6 +124,45 @@ kronq_status dequant_matvec(cudaStream_t st, const kronq_opts &o, const void *de
                             int64_t d_out, int64_t d_in, const float *x, int64_t B, float *y,
                             void *ws, int32_t *info);
 
+// ---------------------------------------------------------------- dense
+// A row-major bf16 matrix (stride in elements); p is null for an absent one.
+struct Mat {
+  void *p = nullptr;
+  int64_t ld = 0;
+};
+kronq_status linear_fwd(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out, const Mat &X,
+                        const Mat &W, const float *bias, int act, const Mat &Z, const Mat &R,
+                        const Mat &Y, int32_t *info);
+kronq_status linear_bwd(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out, const Mat &dY,
+                        const Mat &Z, int act, const Mat &X, const Mat &W, const Mat &dZ,
+                        float *db, const Mat &dXr, const Mat &dX, const Mat &dW, int32_t *info);
+kronq_status gated_fwd(cudaStream_t st, int64_t n, int64_t d, int64_t f, const Mat &X,
+                       const Mat &Wg, const Mat &Wu, int act, const Mat &A, const Mat &U,
+                       const Mat &H, int32_t *info);
+kronq_status gated_bwd(cudaStream_t st, int64_t n, int64_t d, int64_t f, const Mat &dH,
+                       const Mat &A, const Mat &U, int act, const Mat &X, const Mat &Wg,
+                       const Mat &Wu, const Mat &Gg, const Mat &Gu, const Mat &dXr,
+                       const Mat &dX, const Mat &dWg, const Mat &dWu, int32_t *info);
+
+// ---------------------------------------------------------------- distillation
+struct DistillArgs {
+  const void *Z;
+  bool z_bf16;
+  int64_t n, vocab, ldz;
+  const void *T;
+  bool t_bf16;
+  const int32_t *idx;
+  int k;
+  int64_t ldt;
+  float tau;
+  const float *weight;  // null: all 1
+  float *loss, *lse;    // loss null: lse is an input (backward alone)
+  void *dZ;             // null: loss alone
+  int64_t lddz;
+  int32_t *info;
+};
+kronq_status distill(cudaStream_t st, const DistillArgs &a);
+
 // ---------------------------------------------------------------- loss
 size_t loss_ws_bytes(int64_t d_out, int64_t d_in);
 kronq_status layer_loss(cudaStream_t st, const float *W_ref,

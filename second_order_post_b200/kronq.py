@@ -33,6 +33,9 @@ KRONQ_ERR_TIMEOUT = 5
 KRONQ_ERR_CUDA = 6
 KRONQ_F32 = 0
 KRONQ_BF16 = 1
+KRONQ_ACT_NONE, KRONQ_ACT_RELU, KRONQ_ACT_SILU, KRONQ_ACT_GELU, KRONQ_ACT_GELU_TANH = range(5)
+KRONQ_ACTS = {"none": KRONQ_ACT_NONE, "relu": KRONQ_ACT_RELU, "silu": KRONQ_ACT_SILU,
+              "gelu": KRONQ_ACT_GELU, "gelu_tanh": KRONQ_ACT_GELU_TANH}
 KRONQ_FLAG_NO_ROT_IN = 0x1
 KRONQ_FLAG_NO_ROT_OUT = 0x2
 KRONQ_FLAG_NO_SCALE = 0x4
@@ -91,6 +94,20 @@ _SIGS = {
     "kronq_gemm_f32": [_p, _i64, _i64, _i64, _f, _p, _i64, ctypes.c_int, _p,
                        _i64, ctypes.c_int, _f, _p, _i64, _p, _sz, _p],
     "kronq_gemm_f32_workspace_bytes": [_i64, _i64, _i64],
+    "kronq_linear": [_p, _p, _i64, _i64, _i64, _p, _i64, _i64, _p, ctypes.c_int, _p, _i64, _p,
+                     _i64, _p, _i64, _p],
+    "kronq_linear_bwd": [_p, _p, _i64, _p, _i64, ctypes.c_int, _p, _i64, _p, _i64, _i64, _i64,
+                         _i64, _p, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p],
+    "kronq_gated": [_p, _p, _i64, _i64, _i64, _p, _p, _i64, _i64, ctypes.c_int, _p, _p, _i64, _p,
+                    _i64, _p],
+    "kronq_gated_bwd": [_p, _p, _i64, _p, _p, _i64, ctypes.c_int, _p, _i64, _p, _p, _i64, _i64,
+                        _i64, _i64, _p, _p, _i64, _p, _i64, _p, _i64, _p, _p, _i64, _p],
+    "kronq_distill_fwd": [_p, _p, ctypes.c_int, _i64, _i64, _i64, _p, ctypes.c_int, _p, _i64,
+                          _i64, _f, _p, _p, _p, _p],
+    "kronq_distill_bwd": [_p, _p, ctypes.c_int, _i64, _i64, _i64, _p, ctypes.c_int, _p, _i64,
+                          _i64, _f, _p, _p, _p, _i64, _p],
+    "kronq_distill_step": [_p, _p, ctypes.c_int, _i64, _i64, _i64, _p, ctypes.c_int, _p, _i64,
+                           _i64, _f, _p, _p, _p, _p, _i64, _p],
     "kronq_workspace_bytes": [ctypes.c_int, _i64, _i64, _OPTS],
     "kronq_allocate_bits": [_p, _p, ctypes.c_int, _d, _p],
     "kronq_status_string": [ctypes.c_int],
@@ -275,6 +292,186 @@ def kronq_allocate_bits(scores, numel, avg_budget):
         ctypes.cast(s, _p), ctypes.cast(m, _p), n, float(avg_budget),
         ctypes.cast(out, _p)))
     return list(out)
+
+
+# ---------------------------------------------------------------- calibration pass
+# Matrices are 2-D CUDA tensors with contiguous rows (stride(1) == 1); their
+# row strides are the library's leading dimensions. All tensors of a call lie
+# on one device, which need not be the current one; without ``stream`` the
+# call goes to that device's current stream.
+def _view(name, t, rows, cols, dev, dtype=torch.bfloat16):
+    """(pointer, row stride) of an optional matrix, checked."""
+    if t is None:
+        return None, cols + 7 & -8
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {rows} x {cols}, not {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{name} must have contiguous rows, not strides {(s0, s1)}")
+    return t.data_ptr(), (s0 if rows > 1 else cols + 7 & -8)
+
+
+def _vector(name, t, n, dev, dtype=torch.float32):
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be {n} contiguous values, not {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    return t.data_ptr()
+
+
+def _info(info, dev):
+    if info.dtype != torch.int32 or info.numel() < 1 or info.device != dev:
+        raise ValueError(f"info must be an int32 word on {dev}")
+    return info.data_ptr()
+
+
+def _device(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    return t.device
+
+
+def _enqueue(fn, dev, stream, *args):
+    """Calls the library with `dev` current, on `stream` or dev's current one."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, not on {dev}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _enqueue(fn, dev, stream, *args)
+    st = torch.cuda.current_stream() if stream is None else stream
+    status = getattr(_lib, fn)(st.cuda_stream, *args)
+    if status != KRONQ_OK:
+        raise KronqError(fn, status)
+
+
+def kronq_linear(X, W, Y, info, bias=None, act=KRONQ_ACT_NONE, Z=None, R=None, stream=None):
+    """Y = act(X Wᵀ + bias) + R for bf16 X (n x d_in), W (d_out x d_in), R and
+    Y (n x d_out; R may be Y), fp32 bias (d_out). Z (n x d_out), if given,
+    receives the pre-activations. info, an int32 word, is written on failure
+    only."""
+    dev = _device(X, "X")
+    n, d_in = X.shape
+    d_out = W.shape[0]
+    x, w = _view("X", X, n, d_in, dev), _view("W", W, d_out, d_in, dev)
+    z, r = _view("Z", Z, n, d_out, dev), _view("R", R, n, d_out, dev)
+    y = _view("Y", Y, n, d_out, dev)
+    _enqueue("kronq_linear", dev, stream, x[0], n, d_in, x[1], w[0], d_out, w[1],
+             _vector("bias", bias, d_out, dev), act, z[0], z[1], r[0], r[1], y[0], y[1],
+             _info(info, dev))
+
+
+def kronq_linear_bwd(dY, X, W, info, act=KRONQ_ACT_NONE, Z=None, dZ=None, db=None, dX=None,
+                     dXr=None, dW=None, stream=None):
+    """dZ = dY * act'(Z) (the sublayer's G), db = sum of dZ's rows (fp32),
+    dX = dZ W + dXr, dW = dZᵀ X; each output but dZ is optional, and so are
+    dZ and Z with KRONQ_ACT_NONE, X without dW, W without dX (one of X and dX,
+    or W, gives d_in)."""
+    dev = _device(dY, "dY")
+    n, d_out = dY.shape
+    d_in = next((t.shape[1] for t in (X, W, dX, dW) if t is not None), None)
+    if d_in is None:
+        raise ValueError("one of X, W, dX and dW has to give d_in")
+    dy, z = _view("dY", dY, n, d_out, dev), _view("Z", Z, n, d_out, dev)
+    x, w = _view("X", X, n, d_in, dev), _view("W", W, d_out, d_in, dev)
+    dz, dxr = _view("dZ", dZ, n, d_out, dev), _view("dXr", dXr, n, d_in, dev)
+    dx, dw = _view("dX", dX, n, d_in, dev), _view("dW", dW, d_out, d_in, dev)
+    _enqueue("kronq_linear_bwd", dev, stream, dy[0], dy[1], z[0], z[1], act, x[0], x[1], w[0],
+             w[1], n, d_in, d_out, dz[0], dz[1], _vector("db", db, d_out, dev), dxr[0], dxr[1],
+             dx[0], dx[1], dw[0], dw[1], _info(info, dev))
+
+
+def _pair(name, a, b):
+    """The common row stride of two matrices that are given together."""
+    if (a[0] is None) != (b[0] is None):
+        raise ValueError(f"{name} are given together or not at all")
+    if a[1] != b[1]:
+        raise ValueError(f"{name} must have the same row stride")
+    return a[1]
+
+
+def kronq_gated(X, Wg, Wu, H, info, act=KRONQ_ACT_SILU, A=None, U=None, stream=None):
+    """H = act(X Wgᵀ) * (X Wuᵀ) for bf16 X (n x d), Wg and Wu (f x d, the same
+    row stride), H (n x f). A and U (n x f), if given, receive the two products
+    for kronq_gated_bwd."""
+    dev = _device(X, "X")
+    n, d = X.shape
+    f = Wg.shape[0]
+    x, h = _view("X", X, n, d, dev), _view("H", H, n, f, dev)
+    wg, wu = _view("Wg", Wg, f, d, dev), _view("Wu", Wu, f, d, dev)
+    a, u = _view("A", A, n, f, dev), _view("U", U, n, f, dev)
+    _enqueue("kronq_gated", dev, stream, x[0], n, d, x[1], wg[0], wu[0], f,
+             _pair("Wg and Wu", wg, wu), act, a[0], u[0], _pair("A and U", a, u), h[0], h[1],
+             _info(info, dev))
+
+
+def kronq_gated_bwd(dH, A, U, X, Wg, Wu, Gg, Gu, info, act=KRONQ_ACT_SILU, dX=None, dXr=None,
+                    dWg=None, dWu=None, stream=None):
+    """Gg = dH * U * act'(A) and Gu = dH * act(A) (the G of gate and up),
+    dX = Gg Wg + Gu Wu + dXr, dWg = Ggᵀ X, dWu = Guᵀ X; dX and the weight
+    gradients are optional (X may be None without the latter, Wg and Wu
+    without dX)."""
+    dev = _device(dH, "dH")
+    n, f = dH.shape
+    d = next((t.shape[1] for t in (X, Wg, dX, dWg) if t is not None), 1)
+    dh, a, u = (_view(m, t, n, f, dev) for m, t in (("dH", dH), ("A", A), ("U", U)))
+    x, wg, wu = _view("X", X, n, d, dev), _view("Wg", Wg, f, d, dev), _view("Wu", Wu, f, d, dev)
+    gg, gu = _view("Gg", Gg, n, f, dev), _view("Gu", Gu, n, f, dev)
+    dx, dxr = _view("dX", dX, n, d, dev), _view("dXr", dXr, n, d, dev)
+    dwg, dwu = _view("dWg", dWg, f, d, dev), _view("dWu", dWu, f, d, dev)
+    _enqueue("kronq_gated_bwd", dev, stream, dh[0], dh[1], a[0], u[0], _pair("A and U", a, u),
+             act, x[0], x[1], wg[0], wu[0], _pair("Wg and Wu", wg, wu), n, d, f, gg[0], gu[0],
+             _pair("Gg and Gu", gg, gu), dxr[0], dxr[1], dx[0], dx[1], dwg[0], dwu[0],
+             _pair("dWg and dWu", dwg, dwu), _info(info, dev))
+
+
+def _distill_args(Z, T, idx, tau, weight, dev):
+    n, vocab = Z.shape
+    k = T.shape[1]
+    z, t = _view("Z", Z, n, vocab, dev, Z.dtype), _view("T", T, n, k, dev, T.dtype)
+    i = _view("idx", idx, n, k, dev, torch.int32)
+    if n > 1 and t[1] != i[1]:
+        raise ValueError("T and idx must have the same row stride")
+    return (z[0], _dtype(Z), n, vocab, max(z[1], vocab), t[0], _dtype(T), i[0], k, t[1], tau,
+            _vector("weight", weight, n, dev))
+
+
+def kronq_distill_fwd(Z, T, idx, loss, lse, info, tau=1.0, weight=None, stream=None):
+    """loss and lse (n fp32 values) of student logits Z (n x vocab, fp32 or
+    bf16) against a teacher's top logits T (n x k, fp32 or bf16) at the places
+    idx (n x k int32, negative: padding). Rows of weight 0 do not count."""
+    dev = _device(Z, "Z")
+    n = Z.shape[0]
+    _enqueue("kronq_distill_fwd", dev, stream, *_distill_args(Z, T, idx, tau, weight, dev),
+             _vector("loss", loss, n, dev), _vector("lse", lse, n, dev), _info(info, dev))
+
+
+def kronq_distill_bwd(Z, T, idx, lse, dZ, info, tau=1.0, weight=None, stream=None):
+    """dZ (like Z; may be Z) = the gradient of sum(weight * loss), from
+    kronq_distill_fwd's lse."""
+    dev = _device(Z, "Z")
+    n, vocab = Z.shape
+    dz = _view("dZ", dZ, n, vocab, dev, Z.dtype)
+    _enqueue("kronq_distill_bwd", dev, stream, *_distill_args(Z, T, idx, tau, weight, dev),
+             _vector("lse", lse, n, dev), dz[0], max(dz[1], vocab), _info(info, dev))
+
+
+def kronq_distill_step(Z, T, idx, loss, lse, dZ, info, tau=1.0, weight=None, stream=None):
+    """kronq_distill_fwd and kronq_distill_bwd in one pass over the logits;
+    lse may be None."""
+    dev = _device(Z, "Z")
+    n, vocab = Z.shape
+    dz = _view("dZ", dZ, n, vocab, dev, Z.dtype)
+    _enqueue("kronq_distill_step", dev, stream, *_distill_args(Z, T, idx, tau, weight, dev),
+             _vector("loss", loss, n, dev), _vector("lse", lse, n, dev), dz[0],
+             max(dz[1], vocab), _info(info, dev))
 
 
 def kronq_status_string(status):

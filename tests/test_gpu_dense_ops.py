@@ -1,0 +1,421 @@
+"""kronq_linear, kronq_gated and their backward passes against plain fp64
+forms of the same inputs, at sizes where tiles, k-slabs and vectors end
+inside, with strided inputs and outputs whose padding must stay untouched.
+
+Tolerances: bf16 operands make the products exact in fp32, so a result is off
+by the accumulation bound of ops_helpers.acc_bound, the activation's own
+rounding (relative 2^-20 of the value plus what the argument's error moves it:
+|act'| <= 1.13) and half a bf16 step of the stored value."""
+import math
+
+import pytest
+import torch
+
+from ops_helpers import ACTS, HALF_BF16, U32, acc_bound, act64, close, kq, matrix, out_like, \
+    untouched
+
+pytestmark = pytest.mark.gpu
+LIP = 1.13            # largest |act'| of the activations here
+EVAL = 2.0 ** -20     # relative error of an activation's evaluation in fp32
+
+# n, d_in, d_out: tiles are 128 or 256 wide and deep, k-slabs 64, vectors 8
+SIZES = [
+    (1, 1, 1), (1, 64, 128), (2, 8, 7), (3, 65, 257), (17, 200, 130), (33, 1024, 384),
+    (64, 129, 512), (65, 640, 100), (127, 63, 129), (128, 128, 256), (129, 192, 255),
+    (200, 1000, 264), (256, 320, 1024), (257, 72, 513), (600, 520, 700), (1025, 96, 260),
+]
+
+
+def _info():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("act", ACTS)
+def test_linear(cuda_device, size, act):
+    K = kq()
+    n, d_in, d_out = size
+    seed = n * 7 + d_in * 3 + d_out
+    bias_on, res_on, keep = seed % 2 == 0, seed % 3 != 0, act != "none"
+    X, W = matrix(n, d_in, seed, pad=1), matrix(d_out, d_in, seed + 1, 1.3 / math.sqrt(d_in))
+    g = torch.Generator().manual_seed(seed + 2)
+    bias = torch.randn(d_out, generator=g).cuda() if bias_on else None
+    R = matrix(n, d_out, seed + 3, 2.0, pad=2) if res_on else None
+    Y, ybuf = out_like(n, d_out, pad=1)
+    Z, zbuf = out_like(n, d_out) if keep else (None, None)
+    info = _info()
+    K.kronq_linear(X, W, Y, info, bias=bias, act=K.KRONQ_ACTS[act], Z=Z, R=R)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    x, w = X.double(), W.double()
+    z = x @ w.T + (bias.double() if bias_on else 0)
+    e = acc_bound(x, w) + U32 * z.abs() * 2
+    y = act64(z, act)[0]
+    ey = LIP * e + EVAL * y.abs() + 1e-30
+    if res_on:
+        y = y + R.double()
+        ey = ey + U32 * y.abs()
+    close(Y, y, ey + HALF_BF16 * (y.abs() + ey))
+    assert untouched(ybuf, d_out)
+    if keep:
+        close(Z, z, e + HALF_BF16 * (z.abs() + e) + 1e-30)
+        assert untouched(zbuf, d_out)
+
+
+def test_linear_in_place_residual(cuda_device):
+    K = kq()
+    n, d_in, d_out = 300, 256, 392
+    X, W = matrix(n, d_in, 1), matrix(d_out, d_in, 2, 0.08)
+    R = matrix(n, d_out, 3, pad=1)
+    want, _ = out_like(n, d_out)
+    info = _info()
+    K.kronq_linear(X, W, want, info, R=R)
+    K.kronq_linear(X, W, R, info, R=R)
+    torch.cuda.synchronize()
+    assert info.item() == 0 and torch.equal(want, R)
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("act", ACTS)
+def test_linear_bwd(cuda_device, size, act):
+    K = kq()
+    n, d_in, d_out = size
+    seed = n * 5 + d_in + d_out * 3
+    dY, Z = matrix(n, d_out, seed, 0.01, pad=1), matrix(n, d_out, seed + 1, 1.5)
+    X, W = matrix(n, d_in, seed + 2), matrix(d_out, d_in, seed + 3, 0.05, pad=1)
+    dXr = matrix(n, d_in, seed + 4) if seed % 2 else None
+    dZ, zbuf = out_like(n, d_out, pad=1)
+    dX, xbuf = out_like(n, d_in)
+    dW, wbuf = out_like(d_out, d_in, pad=1)
+    db = torch.full((d_out,), 5.0, device="cuda")
+    info = _info()
+    K.kronq_linear_bwd(dY, X, W, info, act=K.KRONQ_ACTS[act], Z=Z, dZ=dZ, db=db, dX=dX, dXr=dXr,
+                       dW=dW)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    da = act64(Z.double(), act)[1]
+    dz = dY.double() * da
+    # |act'| evaluates to 2^-20 relative to its largest term (<= 1.13)
+    ez = EVAL * LIP * dY.double().abs() + U32 * dz.abs()
+    close(dZ, dz, ez + HALF_BF16 * (dz.abs() + ez) + 1e-30)
+    # fp32 sums of at most n terms
+    close(db, dz.sum(0), ez.sum(0) + (n + 2) * U32 * dz.abs().sum(0) + 1e-30)
+    # the products take dZ as it was rounded
+    dzr, w, x = dZ.double(), W.double(), X.double()
+    want = dzr @ w + (dXr.double() if dXr is not None else 0)
+    e = acc_bound(dzr, w.T) + U32 * want.abs()
+    close(dX, want, e + HALF_BF16 * (want.abs() + e) + 1e-30)
+    want = dzr.T @ x
+    e = acc_bound(dzr.T, x.T)
+    close(dW, want, e + HALF_BF16 * (want.abs() + e) + 1e-30)
+    assert untouched(zbuf, d_out) and untouched(xbuf, d_in) and untouched(wbuf, d_in)
+
+
+def test_linear_bwd_without_activation(cuda_device):
+    """dZ absent, dZ = dY and a copied dZ give the same gradients; dZ over Z
+    with an activation too."""
+    K = kq()
+    n, d_in, d_out = 150, 200, 136
+    dY, X = matrix(n, d_out, 1, 0.1), matrix(n, d_in, 2)
+    W, info = matrix(d_out, d_in, 3, 0.1), _info()
+    got = []
+    for dZ in (None, dY, out_like(n, d_out, pad=3)[0]):
+        dX, dW = out_like(n, d_in)[0], out_like(d_out, d_in)[0]
+        db = torch.empty(d_out, device="cuda")
+        K.kronq_linear_bwd(dY, X, W, info, dZ=dZ, db=db, dX=dX, dW=dW)
+        got.append((dX.clone(), dW.clone(), db))
+        if dZ is not None:
+            assert torch.equal(dZ, dY)
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+    Z = matrix(n, d_out, 4)
+    want, _ = out_like(n, d_out)
+    K.kronq_linear_bwd(dY, X, W, info, act=K.KRONQ_ACT_SILU, Z=Z, dZ=want)
+    K.kronq_linear_bwd(dY, X, W, info, act=K.KRONQ_ACT_SILU, Z=Z, dZ=Z)
+    torch.cuda.synchronize()
+    assert info.item() == 0 and torch.equal(want, Z)
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("act", ACTS)
+def test_gated(cuda_device, size, act):
+    K = kq()
+    n, d, f = size
+    seed = n + d * 2 + f * 5
+    X = matrix(n, d, seed)
+    Wg, Wu = (matrix(f, d, seed + j, 1.3 / math.sqrt(d), pad=1) for j in (1, 2))
+    keep = seed % 2 == 0
+    H, hbuf = out_like(n, f, pad=1)
+    A, abuf = out_like(n, f, pad=2) if keep else (None, None)
+    U, ubuf = out_like(n, f, pad=2) if keep else (None, None)
+    info = _info()
+    K.kronq_gated(X, Wg, Wu, H, info, act=K.KRONQ_ACTS[act], A=A, U=U)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    x, wg, wu = X.double(), Wg.double(), Wu.double()
+    a, u = x @ wg.T, x @ wu.T
+    ea, eu = acc_bound(x, wg) + 1e-30, acc_bound(x, wu) + 1e-30
+    s = act64(a, act)[0]
+    h = s * u
+    es = LIP * ea + EVAL * s.abs()
+    eh = es * (u.abs() + eu) + s.abs() * eu + U32 * h.abs()
+    close(H, h, eh + HALF_BF16 * (h.abs() + eh))
+    assert untouched(hbuf, f)
+    if keep:
+        close(A, a, ea + HALF_BF16 * (a.abs() + ea))
+        close(U, u, eu + HALF_BF16 * (u.abs() + eu))
+        assert untouched(abuf, f) and untouched(ubuf, f)
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_bwd(cuda_device, size, act):
+    K = kq()
+    n, d, f = size
+    seed = n * 2 + d + f * 7
+    dH, A, U = matrix(n, f, seed, 0.01), matrix(n, f, seed + 1, 1.5), matrix(n, f, seed + 2)
+    X = matrix(n, d, seed + 3, pad=1)
+    Wg, Wu = matrix(f, d, seed + 4, 0.05), matrix(f, d, seed + 5, 0.05)
+    dXr = matrix(n, d, seed + 6) if seed % 2 else None
+    Gg, gbuf = out_like(n, f, pad=1)
+    Gu, ubuf = out_like(n, f, pad=1)
+    dX, xbuf = out_like(n, d)
+    dWg, wgbuf = out_like(f, d)
+    dWu, wubuf = out_like(f, d)
+    info = _info()
+    K.kronq_gated_bwd(dH, A, U, X, Wg, Wu, Gg, Gu, info, act=K.KRONQ_ACTS[act], dX=dX, dXr=dXr,
+                      dWg=dWg, dWu=dWu)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    dh, u = dH.double(), U.double()
+    s, ds = act64(A.double(), act)
+    gg, gu = dh * u * ds, dh * s
+    eg = (EVAL * LIP + 2 * U32) * (dh * u).abs()
+    eu = EVAL * gu.abs() + U32 * gu.abs()
+    close(Gg, gg, eg + HALF_BF16 * (gg.abs() + eg) + 1e-30)
+    close(Gu, gu, eu + HALF_BF16 * (gu.abs() + eu) + 1e-30)
+    ggr, gur, x, wg, wu = (t.double() for t in (Gg, Gu, X, Wg, Wu))
+    want = ggr @ wg + gur @ wu + (dXr.double() if dXr is not None else 0)
+    cat_g, cat_w = torch.cat([ggr, gur], 1), torch.cat([wg, wu], 0)
+    e = acc_bound(cat_g, cat_w.T) + U32 * want.abs()
+    close(dX, want, e + HALF_BF16 * (want.abs() + e) + 1e-30)
+    for got, g in ((dWg, ggr), (dWu, gur)):
+        want = g.T @ x
+        e = acc_bound(g.T, x.T)
+        close(got, want, e + HALF_BF16 * (want.abs() + e) + 1e-30)
+    assert all(untouched(b, f) for b in (gbuf, ubuf))
+    assert all(untouched(b, d) for b in (xbuf, wgbuf, wubuf))
+
+
+def test_gated_slices_of_one_buffer(cuda_device):
+    """gate and up stored as the halves of one weight, A and U as the halves
+    of one buffer, G over A and U in place."""
+    K = kq()
+    n, d, f = 70, 136, 168
+    X, W = matrix(n, d, 1), matrix(2 * f, d, 2, 0.1)
+    AU = torch.empty(n, 2 * f, dtype=torch.bfloat16, device="cuda")
+    H, info = out_like(n, f)[0], _info()
+    K.kronq_gated(X, W[:f], W[f:], H, info, A=AU[:, :f], U=AU[:, f:])
+    H2, A2, U2 = (out_like(n, f)[0] for _ in range(3))
+    K.kronq_gated(X, W[:f].clone(), W[f:].clone(), H2, info, A=A2, U=U2)
+    torch.cuda.synchronize()
+    assert torch.equal(H, H2) and torch.equal(AU[:, :f], A2) and torch.equal(AU[:, f:], U2)
+    dH = matrix(n, f, 5, 0.1)
+    Gg, Gu = out_like(n, f)[0], out_like(n, f)[0]
+    dX, dX2 = out_like(n, d)[0], out_like(n, d)[0]
+    K.kronq_gated_bwd(dH, A2, U2, X, W[:f], W[f:], Gg, Gu, info, dX=dX)
+    K.kronq_gated_bwd(dH, AU[:, :f], AU[:, f:], X, W[:f], W[f:], AU[:, :f], AU[:, f:], info,
+                      dX=dX2)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    assert torch.equal(Gg, AU[:, :f]) and torch.equal(Gu, AU[:, f:]) and torch.equal(dX, dX2)
+
+
+def test_no_tokens(cuda_device):
+    """n = 0: nothing to compute, and the sums over tokens are 0."""
+    K = kq()
+    d_in, d_out = 72, 130
+    e = lambda w: torch.empty(0, w, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    W, info = matrix(d_out, d_in, 1), _info()
+    K.kronq_linear(e(d_in), W, e(d_out), info)
+    dW, buf = out_like(d_out, d_in, pad=1)
+    db = torch.ones(d_out, device="cuda")
+    K.kronq_linear_bwd(e(d_out), e(d_in), W, info, act=K.KRONQ_ACT_SILU, Z=e(d_out), dZ=e(d_out),
+                       db=db, dX=e(d_in), dW=dW)
+    K.kronq_gated(e(d_in), W, W, e(d_out), info)
+    dWg, dWu = out_like(d_out, d_in)[0], out_like(d_out, d_in)[0]
+    K.kronq_gated_bwd(e(d_out), e(d_out), e(d_out), e(d_in), W, W, e(d_out), e(d_out), info,
+                      dWg=dWg, dWu=dWu)
+    torch.cuda.synchronize()
+    assert info.item() == 0 and untouched(buf, d_in)
+    assert not dW.any() and not db.any() and not dWg.any() and not dWu.any()
+
+
+def test_nonfinite_rows_stay_in_their_row(cuda_device):
+    """A NaN or Inf token changes no other token's outputs (padding tokens may
+    hold anything)."""
+    K = kq()
+    for n in (5, 40, 300):
+        d, f = 200, 264
+        X = matrix(n, d, 1)
+        Wg, Wu, info = matrix(f, d, 2, 0.1), matrix(f, d, 3, 0.1), _info()
+        H, H2 = out_like(n, f)[0], out_like(n, f)[0]
+        K.kronq_gated(X, Wg, Wu, H, info)
+        X[n // 2] = math.nan
+        X[n - 1, 3] = math.inf
+        K.kronq_gated(X, Wg, Wu, H2, info)
+        torch.cuda.synchronize()
+        keep = [r for r in range(n) if r not in (n // 2, n - 1)]
+        assert torch.equal(H[keep], H2[keep]) and bool(H2[n // 2].isnan().all())
+
+
+def test_gradients_against_differences(cuda_device):
+    """dX, dW and db of both operators against central differences of the
+    formulas' loss sum(dY * Y), in fp64."""
+    K = kq()
+    n, d, f, h = 9, 24, 40, 1e-5
+    info = _info()
+    X, W, W2 = matrix(n, d, 1), matrix(f, d, 2, 0.3), matrix(f, d, 3, 0.3)
+    dY = matrix(n, f, 4)
+    bias = torch.randn(f, generator=torch.Generator().manual_seed(5)).cuda()
+    x, w, w2, b, dy = (t.double().cpu() for t in (X, W, W2, bias, dY))
+
+    def diff(fn, t, at):
+        p, m = t.clone(), t.clone()
+        p[at] += h
+        m[at] -= h
+        return float(fn(p) - fn(m)) / (2 * h)
+
+    for act in ("silu", "gelu", "gelu_tanh"):
+        # linear
+        Y, Z, dZ, dX, = (out_like(n, c)[0] for c in (f, f, f, d))
+        dW, db = out_like(f, d)[0], torch.empty(f, device="cuda")
+        K.kronq_linear(X, W, Y, info, bias=bias, act=K.KRONQ_ACTS[act], Z=Z)
+        K.kronq_linear_bwd(dY, X, W, info, act=K.KRONQ_ACTS[act], Z=Z, dZ=dZ, db=db, dX=dX, dW=dW)
+        # gated
+        H, A, U, Gg, Gu = (out_like(n, f)[0] for _ in range(5))
+        eX, eWg, eWu = out_like(n, d)[0], out_like(f, d)[0], out_like(f, d)[0]
+        K.kronq_gated(X, W, W2, H, info, act=K.KRONQ_ACTS[act], A=A, U=U)
+        K.kronq_gated_bwd(dY, A, U, X, W, W2, Gg, Gu, info, act=K.KRONQ_ACTS[act], dX=eX, dWg=eWg,
+                          dWu=eWu)
+        torch.cuda.synchronize()
+        lin = lambda x_, w_, b_: (dy * act64(x_ @ w_.T + b_, act)[0]).sum()  # noqa: E731
+        gat = lambda x_, g_, u_: (dy * act64(x_ @ g_.T, act)[0] * (x_ @ u_.T)).sum()  # noqa: E731
+        checks = [
+            (dX, x, lambda t: lin(t, w, b)), (dW, w, lambda t: lin(x, t, b)),
+            (db, b, lambda t: lin(x, w, t)), (eX, x, lambda t: gat(t, w, w2)),
+            (eWg, w, lambda t: gat(x, t, w2)), (eWu, w2, lambda t: gat(x, w, t)),
+        ]
+        for got, t, fn in checks:
+            got = got.double().cpu()
+            # kept pre-activations, G and the result are rounded to bf16
+            # (three half steps, act'' <= 1.2 on the first): within 2 % of the
+            # largest entry
+            tol = 0.02 * float(got.abs().max())
+            for at in [(0,) * t.dim(), tuple(s - 1 for s in t.shape), tuple(s // 2 for s in t.shape)]:
+                assert abs(float(got[at]) - diff(fn, t, at)) <= tol, (act, at)
+
+
+def test_another_stream_and_no_stream_argument(cuda_device):
+    K = kq()
+    n, d_in, d_out = 64, 512, 512
+    X, W = matrix(n, d_in, 1), matrix(d_out, d_in, 2, 0.05)
+    want, _ = out_like(n, d_out)
+    info = _info()
+    K.kronq_linear(X, W, want, info)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    a, b = out_like(n, d_out)[0], out_like(n, d_out)[0]
+    side.wait_stream(torch.cuda.current_stream())
+    K.kronq_linear(X, W, a, info, stream=side)
+    with torch.cuda.stream(side):
+        K.kronq_linear(X, W, b, info)
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want)
+
+
+def test_captured_and_replayed(cuda_device):
+    """Forward and backward in a CUDA graph, replayed on new inputs, give the
+    eager results; a second graph of the same calls shares nothing with it."""
+    K = kq()
+    n, d, f = 130, 256, 384
+    X, Wg, Wu = matrix(n, d, 1), matrix(f, d, 2, 0.08), matrix(f, d, 3, 0.08)
+    dH, info = matrix(n, f, 4, 0.1), _info()
+
+    def buffers():
+        return [out_like(n, f)[0] for _ in range(5)] + [out_like(n, d)[0]] + \
+            [out_like(f, d)[0] for _ in range(2)]
+
+    def go(b):
+        H, A, U, Gg, Gu, dX, dWg, dWu = b
+        K.kronq_gated(X, Wg, Wu, H, info, A=A, U=U)
+        K.kronq_gated_bwd(dH, A, U, X, Wg, Wu, Gg, Gu, info, dX=dX, dWg=dWg, dWu=dWu)
+
+    eager, one, two = buffers(), buffers(), buffers()
+    go(eager)
+    torch.cuda.synchronize()
+    graphs = []
+    for b in (one, two):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            go(b)
+        graphs.append(g)
+    X.copy_(matrix(n, d, 9))
+    go(eager)
+    for g in graphs + graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    for a, b, c in zip(eager, one, two):
+        assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_same_bits_twice(cuda_device):
+    K = kq()
+    n, d_in, d_out = 48, 2048, 640
+    X, W, info = matrix(n, d_in, 1), matrix(d_out, d_in, 2, 0.05), _info()
+    dY = matrix(n, d_out, 3)
+    runs = []
+    for _ in range(2):
+        Y, dX, dW = out_like(n, d_out)[0], out_like(n, d_in)[0], out_like(d_out, d_in)[0]
+        db = torch.empty(d_out, device="cuda")
+        K.kronq_linear(X, W, Y, info)
+        K.kronq_linear_bwd(dY, X, W, info, db=db, dX=dX, dW=dW)
+        runs.append((Y, dX, dW, db))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+def test_binding_refuses(cuda_device):
+    K = kq()
+    n, d_in, d_out = 8, 64, 32
+    X, W, Y, info = matrix(n, d_in, 1), matrix(d_out, d_in, 2), out_like(n, d_out)[0], _info()
+    with pytest.raises(TypeError):
+        K.kronq_linear(X.float(), W, Y, info)
+    with pytest.raises(ValueError):
+        K.kronq_linear(X, W, Y[:, :31], info)
+    with pytest.raises(ValueError):
+        K.kronq_linear(X, W.T.contiguous().T, Y, info)      # rows not contiguous
+    with pytest.raises(ValueError):
+        K.kronq_linear(X.cpu(), W, Y, info)
+    with pytest.raises(ValueError):
+        K.kronq_linear(X, W.cpu(), Y, info)
+    with pytest.raises(ValueError):
+        K.kronq_linear(X, W, Y, info, bias=torch.zeros(d_out + 1, device="cuda"))
+    with pytest.raises(TypeError):
+        K.kronq_linear(X, W, Y, info, bias=torch.zeros(d_out, device="cuda").half())
+    with pytest.raises(K.KronqError) as err:                # odd row stride
+        K.kronq_linear(torch.zeros(n, 65, dtype=torch.bfloat16, device="cuda")[:, :64], W, Y, info)
+    assert err.value.status == K.KRONQ_ERR_UNSUPPORTED
+    with pytest.raises(K.KronqError) as err:                # Y over X
+        K.kronq_linear(X, matrix(d_in, d_in, 3), X, info)
+    assert err.value.status == K.KRONQ_ERR_INVALID_ARG
+    with pytest.raises(K.KronqError) as err:                # no Z for the derivative
+        K.kronq_linear_bwd(Y, X, W, info, act=K.KRONQ_ACT_GELU, dZ=out_like(n, d_out)[0])
+    assert err.value.status == K.KRONQ_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        K.kronq_gated(X, W, matrix(d_out, d_in, 2, pad=1), Y, info)   # strides differ
+    with pytest.raises(ValueError):
+        K.kronq_gated(X, W, W, Y, info, A=out_like(n, d_out)[0])      # A without U
+    torch.cuda.synchronize()
+    assert info.item() == 0

@@ -1,0 +1,306 @@
+"""kronq_distill_fwd / _bwd / _step against the definition in fp64: padded
+and repeated places, rows that do not count, infinities and NaN, odd widths
+and strides, both logit types.
+
+Bounds. A row's exponentials are off by (2 + |arg|) 2^-23 relative (the
+argument is rounded once, base-2 exponentials are good to 2 ulp), their fp32
+sum by the depth of its tree; lse and loss are fp64 from there."""
+import math
+
+import pytest
+import torch
+
+from ops_helpers import HALF_BF16, U32, close, kq
+
+pytestmark = pytest.mark.gpu
+
+# n, vocab, k
+SIZES = [(1, 1, 1), (2, 7, 3), (5, 33, 33), (3, 1000, 16), (2, 4099, 64), (4, 8192, 1),
+         (2, 32000, 100), (2, 50257, 17), (1, 65537, 1024), (2, 128256, 64), (1, 300001, 8)]
+
+
+def _case(n, vocab, k, dtype, seed, tdtype=torch.float32, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    z = (torch.randn(n, vocab, generator=g, dtype=torch.float64) * 3).to(dtype)
+    Z = torch.full((n, vocab + pad), math.nan, dtype=dtype)
+    Z[:, :vocab] = z
+    idx = torch.stack([torch.randperm(vocab, generator=g)[:k] for _ in range(n)])
+    T = z.gather(1, idx).float() + torch.randn(n, k, generator=g)
+    w = torch.rand(n, generator=g) + 0.1
+    return (Z.cuda()[:, :vocab], T.to(tdtype).cuda(), idx.int().cuda(), w.cuda())
+
+
+def _want(Z, T, idx, tau, w):
+    """(loss, lse, dZ, q, p per entry) in fp64 from the definition."""
+    z, t, n = Z.double(), T.double(), Z.shape[0]
+    kept = (idx >= 0) & (idx < Z.shape[1]) & (t != -math.inf)
+    counts = kept.any(1) & (w != 0)
+    at = torch.where(kept, idx, 0).long()
+    p = torch.softmax(torch.where(kept, t / tau, -math.inf), 1)
+    p = torch.where(kept & counts[:, None], p, 0.0)
+    m = z.amax(1, keepdim=True)
+    lse = m[:, 0] / tau + ((z - m) / tau).exp().sum(1).log()
+    logq = z / tau - lse[:, None]
+    terms = torch.where(p > 0, p * (p.log() - logq.gather(1, at)), 0.0)
+    loss = tau ** 2 * terms.sum(1)
+    q = logq.exp()
+    dz = w.double()[:, None] * tau * (q.scatter_add(1, at, -p))
+    zero = torch.zeros((), dtype=torch.float64, device=Z.device)
+    return (torch.where(counts, loss, zero), torch.where(counts, lse, zero),
+            torch.where(counts[:, None], dz, zero), q, p, logq, counts)
+
+
+def _bounds(Z, T, idx, tau, w, want):
+    loss, lse, dz, q, p, logq, counts = want
+    vocab, k = Z.shape[1], T.shape[1]
+    # one exponential; the sum of them adds at most vocab / 256 + 32 roundings
+    arg = logq.abs().clamp_max(200) * 1.4427
+    e_exp = (3 + arg) * 2.0 ** -23
+    e_lse = (q * e_exp).sum(1) + (vocab / 256 + 32) * U32
+    b_lse = e_lse + U32 * lse.abs() * 2
+    t = T.double()
+    tm = torch.where(torch.isfinite(t), t, -1e30).amax(1, keepdim=True)
+    e_p = (4 + k / 256 + ((t - tm).abs() / tau).clamp_max(200) * 2) * 2.0 ** -23
+    at = idx.clamp(0, vocab - 1).long()
+    gap = torch.where(p > 0, p.clamp_min(1e-300).log() - logq.gather(1, at), 0.0).abs()
+    b_loss = tau ** 2 * (e_lse + (p * (e_p * (gap + 1))).sum(1) * 2) + U32 * 2 * loss.abs()
+    step = HALF_BF16 if Z.dtype == torch.bfloat16 else U32
+    # lse is stored in fp32 between the separate calls
+    dq = q * (e_exp + e_lse[:, None] + 2 * U32 * lse.abs()[:, None] + 4 * U32)
+    dq = dq.scatter_add(1, at, p * (e_p + 2 * U32) * (1 + k * U32))
+    b_dz = (w.double() * tau)[:, None].abs() * dq
+    # results that underflow (2^-126) may be flushed
+    return (b_loss + 1e-37, b_lse + 1e-37,
+            b_dz + step * (dz.abs() + b_dz) + 4 * U32 * dz.abs() + 1e-37)
+
+
+def _run(Z, T, idx, tau, w, fused):
+    K = kq()
+    n, dev = Z.shape[0], Z.device
+    loss, lse = torch.full((n,), 9.0, device=dev), torch.full((n,), 9.0, device=dev)
+    buf = torch.full((n, Z.shape[1] + 5), 77.0, dtype=Z.dtype, device=dev)
+    dZ = buf[:, :Z.shape[1]]
+    info = torch.zeros(1, dtype=torch.int32, device=dev)
+    if fused:
+        K.kronq_distill_step(Z, T, idx, loss, lse, dZ, info, tau=tau, weight=w)
+    else:
+        K.kronq_distill_fwd(Z, T, idx, loss, lse, info, tau=tau, weight=w)
+        K.kronq_distill_bwd(Z, T, idx, lse, dZ, info, tau=tau, weight=w)
+    torch.cuda.synchronize()
+    assert bool((buf[:, Z.shape[1]:] == 77).all())
+    return loss, lse, dZ, info.item()
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("fused", [True, False])
+def test_distill(cuda_device, size, dtype, fused):
+    n, vocab, k = size
+    tau = 0.5 + (vocab % 7) * 0.4
+    Z, T, idx, w = _case(n, vocab, k, dtype, seed=vocab + k,
+                         tdtype=torch.bfloat16 if k % 2 else torch.float32, pad=vocab % 5)
+    if k > 4:
+        idx[:, k // 2] = -1                      # padding inside the row
+        idx[0, -1] = idx[0, 0]                   # the same place twice
+    loss, lse, dZ, info = _run(Z, T, idx, tau, w, fused)
+    assert info == 0
+    want = _want(Z, T, idx, tau, w)
+    b_loss, b_lse, b_dz = _bounds(Z, T, idx, tau, w, want)
+    close(loss, want[0], b_loss)
+    close(lse, want[1], b_lse)
+    close(dZ, want[2], b_dz)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [321, 40000])
+def test_rows_that_do_not_count(cuda_device, dtype, vocab):
+    """Weight 0 (with NaN logits), nothing kept, teacher logits of -inf, and
+    -inf student logits away from the teacher's places."""
+    n, k = 6, 9
+    Z, T, idx, w = _case(n, vocab, k, dtype, seed=3)
+    w[1] = 0
+    Z[1] = math.nan
+    idx[2] = -1
+    T[3] = -math.inf
+    T[4, 2:] = -math.inf
+    named = torch.zeros(vocab, dtype=torch.bool, device="cuda")
+    named[idx[5].long()] = True
+    Z[5, ~named & (torch.arange(vocab, device="cuda") % 3 != 0)] = -math.inf
+    want = _want(Z, T, idx, 1.5, w)
+    b = _bounds(Z, T, idx, 1.5, w, want)
+    for fused in (True, False):
+        loss, lse, dZ, info = _run(Z, T, idx, 1.5, w, fused)
+        assert info == 0
+        for r in (1, 2, 3):
+            assert loss[r] == 0 and lse[r] == 0 and not dZ[r].any()
+        for r in (0, 4, 5):
+            close(loss[r], want[0][r], b[0][r])
+            close(lse[r], want[1][r], b[1][r])
+            close(dZ[r], want[2][r], b[2][r])
+        assert not dZ[5][Z[5] == -math.inf].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_nonfinite_is_reported(cuda_device, dtype):
+    """A NaN logit, a row of -inf, and a student -inf where the teacher has
+    weight: reported, and the other rows are as without them."""
+    K = kq()
+    n, vocab, k = 4, 777, 5
+    Z, T, idx, w = _case(n, vocab, k, dtype, seed=8)
+    clean = _run(Z, T, idx, 1.0, w, True)
+    assert clean[3] == 0
+    for kind in ("nan", "row", "place"):
+        Z2 = Z.clone()
+        if kind == "nan":
+            Z2[2, 100] = math.nan
+        elif kind == "row":
+            Z2[2] = -math.inf
+        else:
+            Z2[2, idx[2, 1].item()] = -math.inf
+        for fused in (True, False):
+            loss, lse, dZ, info = _run(Z2, T, idx, 1.0, w, fused)
+            assert info == K.KRONQ_ERR_NONFINITE
+            assert loss[2] == math.inf if kind == "place" else bool(loss[2].isnan())
+            if kind == "place":
+                assert bool(dZ[2].isfinite().all())
+            else:
+                assert bool(dZ[2].isnan().all())
+            keep = [0, 1, 3]
+            if fused:
+                assert torch.equal(loss[keep], clean[0][keep])
+                assert torch.equal(dZ[keep], clean[2][keep])
+
+
+def test_place_outside_the_vocabulary(cuda_device):
+    """Left out like padding, and reported."""
+    K = kq()
+    n, vocab, k = 3, 500, 6
+    Z, T, idx, w = _case(n, vocab, k, torch.float32, seed=4)
+    pad = idx.clone()
+    idx[1, 2], pad[1, 2] = vocab, -1
+    idx[2, 0], pad[2, 0] = 2 ** 31 - 1, -7
+    got, want = _run(Z, T, idx, 2.0, w, True), _run(Z, T, pad, 2.0, w, True)
+    assert got[3] == K.KRONQ_ERR_INVALID_ARG and want[3] == 0
+    assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [1001, 32000, 200000])
+def test_in_place_and_without_weights(cuda_device, dtype, vocab):
+    K = kq()
+    n, k = 3, 12
+    Z, T, idx, _ = _case(n, vocab, k, dtype, seed=6)
+    ones = torch.ones(n, device="cuda")
+    want = _run(Z, T, idx, 1.25, ones, True)
+    split = _run(Z, T, idx, 1.25, ones, False)
+    loss = torch.empty(n, device="cuda")
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    Z2 = Z.clone()
+    K.kronq_distill_step(Z2, T, idx, loss, None, Z2, info, tau=1.25)
+    Z3 = Z.clone()
+    K.kronq_distill_bwd(Z3, T, idx, split[1], Z3, info, tau=1.25)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    assert torch.equal(loss, want[0]) and torch.equal(Z2, want[2])
+    assert torch.equal(Z3, split[2])
+
+
+def test_large_logits_and_temperatures(cuda_device):
+    """Logits of +-1e4 and the temperatures at the ends: a one-hot or a
+    uniform student, no overflow."""
+    n, vocab, k = 2, 600, 4
+    for tau in (1e-4, 0.02, 1e4):
+        Z, T, idx, w = _case(n, vocab, k, torch.float32, seed=2)
+        Z = Z * 3000 if tau < 1 else Z
+        T = T * 3000 if tau < 1 else T
+        loss, lse, dZ, info = _run(Z, T, idx, tau, w, True)
+        want = _want(Z, T, idx, tau, w)
+        assert info == 0
+        # an argument of up to 2^x magnitude is rounded to 2^(x-24) absolute:
+        # scale the row's bounds by it (only the largest terms count)
+        arg = float((Z.double().abs().max() / tau) * 1.4427)
+        slack = 1 + arg * 2.0 ** -20
+        b = _bounds(Z, T, idx, tau, w, want)
+        close(lse, want[1], b[0] * 0 + b[1] * slack + U32 * 4 * want[1].abs())
+        close(loss, want[0], b[0] * slack + 8 * U32 * tau ** 2 * arg)
+        close(dZ, want[2], b[2] * slack + 8 * U32 * arg * 1e-3 * float(w.max()) * tau
+              + 8 * U32 * float(w.max()) * tau)
+
+
+def test_gradient_against_differences(cuda_device):
+    """dZ against central differences of the fp64 loss."""
+    n, vocab, k, tau, h = 2, 50, 6, 1.7, 1e-4
+    Z, T, idx, w = _case(n, vocab, k, torch.float32, seed=12)
+    idx[0, 1] = idx[0, 0]
+    dZ = _run(Z, T, idx, tau, w, True)[2].double()
+
+    def total(z):
+        return float((w.double() * _want(z, T, idx, tau, w)[0]).sum())
+
+    z = Z.double()
+    for r, v in [(0, int(idx[0, 0])), (0, int(idx[0, 3])), (1, int(idx[1, 5])), (1, 0), (0, 49)]:
+        p, m = z.clone(), z.clone()
+        p[r, v] += h
+        m[r, v] -= h
+        # differences: O(h^2) and rounding of fp64 losses; dZ: fp32
+        assert abs(float(dZ[r, v]) - (total(p) - total(m)) / (2 * h)) <= 1e-6
+
+
+def test_streams_graphs_and_repeats(cuda_device):
+    K = kq()
+    n, vocab, k = 40, 9001, 20
+    Z, T, idx, w = _case(n, vocab, k, torch.bfloat16, seed=5)
+    want = _run(Z, T, idx, 1.0, w, True)
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    dZ = torch.empty_like(Z)
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    K.kronq_distill_step(Z, T, idx, loss, lse, dZ, info, weight=w, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(loss, want[0]) and torch.equal(dZ, want[2])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        K.kronq_distill_step(Z, T, idx, loss, lse, dZ, info, weight=w)
+    dZ.zero_()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(loss, want[0]) and torch.equal(dZ, want[2]) and info.item() == 0
+
+
+def test_no_rows(cuda_device):
+    K = kq()
+    e = torch.empty(0, 100, device="cuda")
+    T, idx = torch.empty(0, 3, device="cuda"), torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    v, info = torch.empty(0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    K.kronq_distill_step(e, T, idx, v, v, torch.empty(0, 100, device="cuda"), info)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+
+
+def test_binding_refuses(cuda_device):
+    K = kq()
+    Z, T, idx, w = _case(4, 90, 5, torch.float32, seed=1)
+    loss, lse = torch.empty(4, device="cuda"), torch.empty(4, device="cuda")
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError):
+        K.kronq_distill_fwd(Z, T, idx.long(), loss, lse, info)
+    with pytest.raises(TypeError):
+        K.kronq_distill_fwd(Z.half(), T, idx, loss, lse, info)
+    with pytest.raises(ValueError):
+        K.kronq_distill_fwd(Z, T[:, :4], idx, loss, lse, info)
+    with pytest.raises(ValueError):
+        K.kronq_distill_fwd(Z, T, idx, loss[:3], lse, info)
+    for tau in (0.0, -1.0, math.inf, math.nan, 1e-5):
+        with pytest.raises(K.KronqError) as err:
+            K.kronq_distill_fwd(Z, T, idx, loss, lse, info, tau=tau)
+        assert err.value.status == K.KRONQ_ERR_INVALID_ARG
+    wide = torch.empty(4, 200, device="cuda")
+    with pytest.raises(K.KronqError) as err:     # dZ shifted over Z
+        K.kronq_distill_bwd(wide[:, :90], T, idx, lse, wide[:, 10:100], info)
+    assert err.value.status == K.KRONQ_ERR_INVALID_ARG
+    big = torch.zeros(1, 1025, device="cuda")
+    with pytest.raises(K.KronqError) as err:     # k > 1024
+        K.kronq_distill_fwd(big, big, big.int(), loss[:1], lse[:1], info)
+    assert err.value.status == K.KRONQ_ERR_UNSUPPORTED
