@@ -99,6 +99,28 @@ __device__ __forceinline__ void add32(const __nv_bfloat16 *p, float *v, int n) {
   }
 }
 
+// The epilogue of 32 consecutive columns of a row: v the accumulator (gated: v
+// of the gate, u of the up projection), n of them in range.
+template <bool GATED, int ACT>
+__device__ __forceinline__ void finish32(const DenseP &p, int64_t row, int64_t col, int n,
+                                         float *v, float *u) {
+  if (!GATED && p.bias) {
+#pragma unroll
+    for (int t = 0; t < 32; ++t) v[t] += t < n ? __ldg(p.bias + col + t) : 0.f;
+  }
+  if (p.Z) store32(p.Z + row * p.ldz + col, v, n);
+  if constexpr (GATED) {
+    if (p.Z) store32(p.Z2 + row * p.ldz + col, u, n);
+#pragma unroll
+    for (int t = 0; t < 32; ++t) v[t] = act_f<ACT>(v[t]) * u[t];
+  } else {
+#pragma unroll
+    for (int t = 0; t < 32; ++t) v[t] = act_f<ACT>(v[t]);
+    if (p.R) add32(p.R + row * p.ldr + col, v, n);
+  }
+  store32(p.Y + row * p.ldy + col, v, n);
+}
+
 template <bool GATED, int ACT, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(DTHREADS, 1)
     dense_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -195,22 +217,7 @@ __global__ void __launch_bounds__(DTHREADS, 1)
         float v[32], u[GATED ? 32 : 1];
         tmem_ld32(ta, v);
         if constexpr (GATED) tmem_ld32(ta + DT, u);
-        if (row >= p.M) continue;
-        if (!GATED && p.bias) {
-#pragma unroll
-          for (int t = 0; t < 32; ++t) v[t] += t < n ? __ldg(p.bias + col + t) : 0.f;
-        }
-        if (p.Z) store32(p.Z + row * p.ldz + col, v, n);
-        if constexpr (GATED) {
-          if (p.Z) store32(p.Z2 + row * p.ldz + col, u, n);
-#pragma unroll
-          for (int t = 0; t < 32; ++t) v[t] = act_f<ACT>(v[t]) * u[t];
-        } else {
-#pragma unroll
-          for (int t = 0; t < 32; ++t) v[t] = act_f<ACT>(v[t]);
-          if (p.R) add32(p.R + row * p.ldr + col, v, n);
-        }
-        store32(p.Y + row * p.ldy + col, v, n);
+        if (row < p.M) finish32<GATED, ACT>(p, row, col, n, v, u);
       }
     }
   }
@@ -240,6 +247,218 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tbase, COLS);
+  }
+}
+
+// ---------------------------------------------------------------- CTA pairs
+// The same products on CTA pairs, for many rows: a cluster of two CTAs owns a
+// 256 x 256 tile of D (gated: 256 rows x 128 columns of both products). Each
+// CTA holds 128 rows of A and 128 of the 256 columns' rows of B (gated: the
+// even CTA Wg's, the odd one Wu's), so a k-slab of 64 costs a CTA 32 KB of
+// shared-memory traffic for 128 x 256 x 64 products: half of what one CTA
+// alone would load. The kernel is persistent: TMEM holds two accumulators,
+// and the epilogue of one tile runs while the next one accumulates.
+//   warps 0..7  epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half
+//               w / 4 of the tile's columns
+//   warp 8      TMA producer (each CTA loads its own panels; the bytes of both
+//               are counted on the even CTA's barrier)
+//   warp 9      TMEM owner; in the even CTA the MMA issuer
+constexpr int PSTAGES = 6;
+constexpr int PSTAGE = 2 * DPANEL;
+constexpr int PTHREADS = 320;
+constexpr int PGROUP = 8;                // tile raster: row tiles per band
+
+struct PairCtl {
+  uint64_t full[PSTAGES];    // both CTAs' panels landed (even CTA's is used)
+  uint64_t empty[PSTAGES];   // MMAs that read the stage finished (both CTAs)
+  uint64_t tfull[2];         // accumulator complete (both CTAs)
+  uint64_t tempty[2];        // read out by both CTAs' epilogues (even CTA's)
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr int PSMEM = PSTAGES * PSTAGE + 1024 + int(sizeof(PairCtl)) + 64;
+
+__device__ __forceinline__ void load_panel_pair(uint8_t *dst, const CUtensorMap *map,
+                                                uint32_t bar, bool mn, int32_t r0, int32_t k0) {
+  if (!mn) {
+    tma_load_2d_pair(dst, map, bar, k0, r0);
+  } else {
+    tma_load_2d_pair(dst, map, bar, r0, k0);
+    tma_load_2d_pair(dst + DBOX, map, bar, r0 + 64, k0);
+  }
+}
+
+// Row and column tile of tile t: bands of PGROUP row tiles, column by column,
+// so that the tiles in flight share their panels through L2.
+__device__ __forceinline__ void pair_tile(int64_t t, int tiles_m, int tiles_n, int64_t &bi,
+                                          int64_t &bj) {
+  const int64_t band = t / (int64_t(PGROUP) * tiles_n);
+  const int64_t rows = kq_min<int64_t>(PGROUP, tiles_m - band * PGROUP);
+  const int64_t r = t - band * PGROUP * tiles_n;
+  bi = band * PGROUP + r % rows;
+  bj = r / rows;
+}
+
+template <bool GATED, int ACT, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
+    dense_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmA2,
+                      const __grid_constant__ CUtensorMap tmB2, const DenseP p) {
+  constexpr int NT = GATED ? 128 : 256;   // columns of the output per tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  PairCtl *ctl = reinterpret_cast<PairCtl *>(smem + PSTAGES * PSTAGE);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int64_t cluster = cluster_id_x(), clusters = gridDim.x / 2;
+  const int tiles_n = static_cast<int>((p.N + NT - 1) / NT);
+  const int64_t tiles = int64_t(p.tiles_m) * tiles_n;
+  const int nk = p.nk1 * p.nseg;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < PSTAGES; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&ctl->tfull[a], 1);
+      mbar_init(&ctl->tempty[a], 16);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  __syncthreads();
+  if (warp == 9) tmem_alloc_pair(&ctl->tmem_base, 512);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tbase = ctl->tmem_base;
+  volatile int *abort = &ctl->abort;
+
+  int64_t issued = 0;
+  if (warp == 8) {
+    if (lane == 0) {
+      int64_t g = 0;
+      bool ok = true;
+      for (int64_t t = cluster; t < tiles && ok; t += clusters) {
+        int64_t bi, bj;
+        pair_tile(t, p.tiles_m, tiles_n, bi, bj);
+        const int32_t m0 = static_cast<int32_t>(bi * 256 + 128 * rank);
+        const int32_t n0 = static_cast<int32_t>(bj * NT + (GATED ? 0 : 128 * rank));
+        for (int it = 0; it < nk; ++it, ++g) {
+          const int s = static_cast<int>(g % PSTAGES);
+          if (g >= PSTAGES && !mbar_wait(&ctl->empty[s], ((g / PSTAGES) - 1) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          uint8_t *st = smem + s * PSTAGE;
+          const bool second = it >= p.nk1;
+          const int32_t k0 = (second ? it - p.nk1 : it) * DBK;
+          const uint32_t bar = mapa_shared(smem_u32(&ctl->full[s]), 0);
+          if (rank == 0) mbar_expect_tx(&ctl->full[s], 2 * PSTAGE);
+          load_panel_pair(st, second ? &tmA2 : &tmA, bar, A_MN, m0, k0);
+          load_panel_pair(st + DPANEL, (GATED ? rank != 0 : second) ? &tmB2 : &tmB, bar, B_MN, n0,
+                          k0);
+          issued = g + 1;
+        }
+      }
+      // every arrival on this CTA's barriers has landed before the CTA ends
+      for (int64_t e = kq_max<int64_t>(g - PSTAGES, 0); e < g && ok; ++e)
+        ok = mbar_wait(&ctl->empty[e % PSTAGES], (e / PSTAGES) & 1, abort);
+    }
+  } else if (warp == 9) {
+    if (rank == 0 && lane == 0) {
+      const uint32_t idesc = idesc_make(1, A_MN, B_MN, 256, 256);
+      int64_t g = 0;
+      int i = 0;
+      bool ok = true;
+      for (int64_t t = cluster; t < tiles && ok; t += clusters, ++i) {
+        const int a = i & 1;
+        if (i >= 2 && !mbar_wait(&ctl->tempty[a], ((i >> 1) - 1) & 1, abort)) break;
+        tc_fence_after();
+        for (int it = 0; it < nk; ++it, ++g) {
+          const int s = static_cast<int>(g % PSTAGES);
+          if (!mbar_wait(&ctl->full[s], (g / PSTAGES) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + s * PSTAGE), b0 = a0 + DPANEL;
+#pragma unroll
+          for (int kk = 0; kk < DBK / 16; ++kk) {
+            const uint64_t da = A_MN ? sdesc_sw128(a0 + kk * 2048, DBOX, 1024)
+                                     : sdesc_sw128(a0 + kk * 32, 16, 1024);
+            const uint64_t db = B_MN ? sdesc_sw128(b0 + kk * 2048, DBOX, 1024)
+                                     : sdesc_sw128(b0 + kk * 32, 16, 1024);
+            umma_bf16_pair(tbase + 256 * a, da, db, idesc, (it | kk) != 0);
+          }
+          umma_commit_pair(&ctl->empty[s]);
+        }
+        if (ok) umma_commit_pair(&ctl->tfull[a]);
+      }
+    }
+  } else {
+    const int q = warp & 3, half = warp >> 2;
+    int i = 0;
+    for (int64_t t = cluster; t < tiles; t += clusters, ++i) {
+      const int a = i & 1;
+      const bool ok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      int64_t bi, bj;
+      pair_tile(t, p.tiles_m, tiles_n, bi, bj);
+      const int64_t row = bi * 256 + 128 * rank + 32 * q + lane;
+      for (int c = 0; c < NT / 64; ++c) {
+        const int cc = half * (NT / 2) + 32 * c;
+        const int64_t col = bj * NT + cc;
+        if (col >= p.N) break;
+        const int n = static_cast<int>(kq_min<int64_t>(32, p.N - col));
+        const uint32_t ta = tbase + (static_cast<uint32_t>(32 * q) << 16) + 256 * a + cc;
+        float v[32], u[GATED ? 32 : 1];
+        tmem_ld32(ta, v);
+        if constexpr (GATED) tmem_ld32(ta + 128, u);
+        if (row < p.M) finish32<GATED, ACT>(p, row, col, n, v, u);
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tempty[a]), 0));
+    }
+  }
+
+  // ---- teardown: after an abort make sure no copy or MMA is still in flight
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (ctl->abort) {
+    if (threadIdx.x == 0) report(p.info, KRONQ_ERR_TIMEOUT);
+    if (rank == 0 && warp == 8 && lane == 0) {
+      const uint64_t t0 = globaltimer();
+      for (int s = 0; s < PSTAGES && s < issued; ++s) {
+        const int64_t last = ((issued - 1 - s) / PSTAGES) * PSTAGES + s;
+        while (!mbar_try_wait(&ctl->full[s], (last / PSTAGES) & 1) &&
+               globaltimer() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+    if (rank == 0 && warp == 9 && lane == 0) {
+      umma_commit_pair(&ctl->drain);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(&ctl->drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc_pair(tbase, 512);
   }
 }
 
@@ -362,6 +581,17 @@ kronq_status operand_map(CUtensorMap *m, const void *p, int64_t ld, bool mn, int
 
 template <bool GATED, int ACT, bool A_MN, bool B_MN>
 kronq_status launch_dense(cudaStream_t st, const CUtensorMap *tm, DenseP p) {
+  if (p.M > 128) {
+    auto *kern = dense_pair_kernel<GATED, ACT, A_MN, B_MN>;
+    KQ_TRY(smem_attr(kern, PSMEM));
+    p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
+    const int64_t tiles = p.tiles_m * ceil_div(p.N, GATED ? 128 : 256);
+    const int64_t clusters = kq_min<int64_t>(tiles, 74);
+    kern<<<static_cast<unsigned>(2 * clusters), PTHREADS, PSMEM, st>>>(tm[0], tm[1], tm[2], tm[3],
+                                                                       p);
+    KQ_CHECK_LAUNCH();
+    return KRONQ_OK;
+  }
   auto *kern = dense_kernel<GATED, ACT, A_MN, B_MN>;
   KQ_TRY(smem_attr(kern, dense_smem<GATED>()));
   p.tiles_m = static_cast<int>(ceil_div(p.M, DT));
