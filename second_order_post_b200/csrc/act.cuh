@@ -27,6 +27,17 @@ __device__ __forceinline__ float act_f(float z) {
   return z;
 }
 
+// the same with the activation chosen at run time
+__device__ __forceinline__ float act_run(int act, float z) {
+  switch (act) {
+    case KRONQ_ACT_RELU: return act_f<KRONQ_ACT_RELU>(z);
+    case KRONQ_ACT_SILU: return act_f<KRONQ_ACT_SILU>(z);
+    case KRONQ_ACT_GELU: return act_f<KRONQ_ACT_GELU>(z);
+    case KRONQ_ACT_GELU_TANH: return act_f<KRONQ_ACT_GELU_TANH>(z);
+    default: return z;
+  }
+}
+
 // value and derivative
 template <int ACT>
 __device__ __forceinline__ void act_df(float z, float &h, float &dh) {

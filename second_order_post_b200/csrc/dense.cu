@@ -3,15 +3,14 @@
 //   kronq_gated     H = act(X Wg^T) * (X Wu^T)
 // and the products of their backward passes (dX = dZ W, dW = dZ^T X).
 //
-// One template: D = A B^T (A: M x K, B: N x K, either stored K-major or
-// MN-major) on tcgen05.mma kind::f16, bf16 operands, fp32 accumulator in
-// TMEM. A CTA owns 128 rows of D and 128 columns (gated: the same 128
-// columns of both products, side by side in TMEM, so that one thread holds
-// both factors of an output):
-//   warp 0      TMA producer (one elected lane), 4-stage ring of 64-wide slabs
-//   warp 1      TMEM owner and MMA issuer (one elected lane)
-//   warps 2..5  epilogue: TMEM -> registers -> bias, activation, residual ->
-//               bf16 -> global
+// All of them are D = A B^T (A: M x K, B: N x K, either stored K-major or
+// MN-major) on tcgen05.mma kind::f16, bf16 operands brought in by TMA, fp32
+// accumulators in TMEM, and an epilogue on the way out (bias, activation,
+// product of the pair, residual, one rounding to bf16). Two kernels: CTA pairs
+// on 256 x 256 tiles for many tokens, and a kernel for few tokens that is
+// bound by reading the weights and splits k over the CTAs of a cluster. In
+// both, the gated pair's two products share one pass over X and meet in the
+// epilogue of the thread that holds both factors of an output.
 // dX of the gated pair is one product over K = 2 f: the k-slabs of (Gg, Wg)
 // and then those of (Gu, Wu) go into one accumulator.
 #include <string.h>
@@ -24,13 +23,11 @@ namespace {
 
 constexpr int DT = 128;                  // tile rows and columns
 constexpr int DBK = 64;                  // k per stage
-constexpr int DSTAGES = 4;
-constexpr int DTHREADS = 192;
 constexpr int DPANEL = DT * DBK * 2;     // one operand panel of a stage (bytes)
 constexpr int DBOX = 64 * DBK * 2;       // one MN-major box: 64 x 64
 
 struct DenseP {
-  int64_t M, N;
+  int64_t M, N, K;
   int nk1, nseg;               // k-stages per segment, segments
   int tiles_m;
   const float *bias;           // linear
@@ -42,17 +39,6 @@ struct DenseP {
   int64_t ldy;
   int32_t *info;
 };
-
-struct DenseCtl {
-  uint64_t full[DSTAGES], empty[DSTAGES], done, drain;
-  uint32_t tmem_base;
-  int abort;
-};
-
-template <bool GATED>
-constexpr int dense_smem() {
-  return DSTAGES * DPANEL * (GATED ? 3 : 2) + 1024 + int(sizeof(DenseCtl)) + 64;
-}
 
 __device__ __forceinline__ void load_panel(uint8_t *dst, const CUtensorMap *map, uint64_t *bar,
                                            bool mn, int32_t r0, int32_t k0) {
@@ -121,24 +107,74 @@ __device__ __forceinline__ void finish32(const DenseP &p, int64_t row, int64_t c
   store32(p.Y + row * p.ldy + col, v, n);
 }
 
-template <bool GATED, int ACT, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(DTHREADS, 1)
-    dense_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmA2,
-                 const __grid_constant__ CUtensorMap tmB2, const DenseP p) {
-  constexpr int STAGE = DPANEL * (GATED ? 3 : 2);
-  constexpr int COLS = GATED ? 256 : 128;
+// ---------------------------------------------------------------- few tokens
+// For few tokens the sides change places: 128 weight rows are the MMA's M and
+// up to NT tokens its N, so that a tile wastes no tensor work on absent rows
+// and the weights, which bound the call, stream through one 64-wide slab ring.
+// The k range is split over a cluster of S CTAs (as many as fill the SMs):
+// each accumulates its part in TMEM, writes it to its shared memory as
+// [token][feature], and after a cluster barrier every CTA sums a share of the
+// tile over the S parts, always in the order of their ranks, through
+// distributed shared memory. Warp 0 loads (one lane), warp 1 issues the MMAs
+// (one lane), then all four warps read TMEM and finish the tile.
+constexpr int FTHREADS = 128;
+
+template <bool GATED, int NT>
+struct Few {
+  static constexpr int STAGE = DPANEL * (GATED ? 2 : 1) + NT * 128;
+  // two CTAs an SM where four stages fit in half of it, else one
+  static constexpr int PER_SM = STAGE * 4 <= 108 * 1024 ? 2 : 1;
+  static constexpr int STAGES = (PER_SM == 2 ? 108 : 216) * 1024 / STAGE;
+  static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
+  static constexpr int COLS = (GATED ? 2 : 1) * NT < 32 ? 32 : (GATED ? 2 : 1) * NT;
+  static_assert(STAGES * STAGE >= (GATED ? 2 : 1) * NT * 128 * 4, "parts fit in the ring");
+};
+
+struct FewP {
+  DenseP d;
+  int act, split, tiles_t;   // CTAs per tile, token tiles
+};
+
+template <int STAGES>
+struct FewCtl {
+  uint64_t full[STAGES], empty[STAGES], done, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *v, int n) {
+  if (n >= 4) {
+    __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(o);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (t < n) p[t] = __float2bfloat16_rn(v[t]);
+  }
+}
+
+template <bool GATED, bool W_MN, int NT>
+__global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
+    dense_few_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                     const __grid_constant__ CUtensorMap tmX2,
+                     const __grid_constant__ CUtensorMap tmW2, const FewP fp) {
+  using C = Few<GATED, NT>;
+  const DenseP &p = fp.d;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  DenseCtl *ctl = reinterpret_cast<DenseCtl *>(smem + DSTAGES * STAGE);
+  auto *ctl = reinterpret_cast<FewCtl<C::STAGES> *>(smem + C::STAGES * C::STAGE);
+  static_assert(sizeof(*ctl) <= 256, "control block");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t m0 = int64_t(blockIdx.x % p.tiles_m) * DT;
-  const int64_t n0 = int64_t(blockIdx.x / p.tiles_m) * DT;
-  const int nk = p.nk1 * p.nseg;
+  const int split = fp.split, rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t tile = blockIdx.x / split;
+  const int64_t t0 = tile % fp.tiles_t * NT, f0 = tile / fp.tiles_t * DT;
+  // this CTA's k-slabs
+  const int nk = p.nk1 * p.nseg, base = nk / split, extra = nk % split;
+  const int kb = rank * base + (rank < extra ? rank : extra), cnt = base + (rank < extra ? 1 : 0);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < DSTAGES; ++s) {
+    for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
     }
@@ -148,7 +184,7 @@ __global__ void __launch_bounds__(DTHREADS, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&ctl->tmem_base, COLS);
+    tmem_alloc(&ctl->tmem_base, C::COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -158,95 +194,146 @@ __global__ void __launch_bounds__(DTHREADS, 1)
   volatile int *abort = &ctl->abort;
 
   int issued = 0;
-  if (warp == 0) {
-    if (lane == 0) {
-      for (int it = 0; it < nk; ++it) {
-        const int s = it % DSTAGES;
-        if (it >= DSTAGES && !mbar_wait(&ctl->empty[s], ((it / DSTAGES) - 1) & 1, abort)) break;
-        uint8_t *st = smem + s * STAGE;
-        const bool second = it >= p.nk1;
-        const int32_t k0 = (second ? it - p.nk1 : it) * DBK;
-        mbar_expect_tx(&ctl->full[s], STAGE);
-        load_panel(st, second ? &tmA2 : &tmA, &ctl->full[s], A_MN, static_cast<int32_t>(m0), k0);
-        load_panel(st + DPANEL, !GATED && second ? &tmB2 : &tmB, &ctl->full[s], B_MN,
-                   static_cast<int32_t>(n0), k0);
-        if (GATED)
-          load_panel(st + 2 * DPANEL, &tmB2, &ctl->full[s], B_MN, static_cast<int32_t>(n0), k0);
-        issued = it + 1;
-      }
+  if (warp == 0 && lane == 0) {
+    for (int it = 0; it < cnt; ++it) {
+      const int s = it % C::STAGES;
+      if (it >= C::STAGES && !mbar_wait(&ctl->empty[s], ((it / C::STAGES) - 1) & 1, abort)) break;
+      uint8_t *st = smem + s * C::STAGE;
+      const int kt = kb + it;
+      const bool second = kt >= p.nk1;
+      const int32_t k0 = (second ? kt - p.nk1 : kt) * DBK;
+      mbar_expect_tx(&ctl->full[s], C::STAGE);
+      load_panel(st, !GATED && second ? &tmW2 : &tmW, &ctl->full[s], W_MN,
+                 static_cast<int32_t>(f0), k0);
+      if (GATED) load_panel(st + DPANEL, &tmW2, &ctl->full[s], W_MN, static_cast<int32_t>(f0), k0);
+      tma_load_2d(st + DPANEL * (GATED ? 2 : 1), second ? &tmX2 : &tmX, &ctl->full[s], k0,
+                  static_cast<int32_t>(t0));
+      issued = it + 1;
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_make(1, A_MN, B_MN, DT, DT);
-      bool ok = true;
-      for (int it = 0; it < nk; ++it) {
-        const int s = it % DSTAGES;
-        if (!mbar_wait(&ctl->full[s], (it / DSTAGES) & 1, abort)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t a0 = smem_u32(smem + s * STAGE), b0 = a0 + DPANEL;
-#pragma unroll
-        for (int kk = 0; kk < DBK / 16; ++kk) {
-          const uint64_t da = A_MN ? sdesc_sw128(a0 + kk * 2048, DBOX, 1024)
-                                   : sdesc_sw128(a0 + kk * 32, 16, 1024);
-#pragma unroll
-          for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-            const uint32_t b = b0 + h * DPANEL;
-            const uint64_t db = B_MN ? sdesc_sw128(b + kk * 2048, DBOX, 1024)
-                                     : sdesc_sw128(b + kk * 32, 16, 1024);
-            umma_bf16(tbase + DT * h, da, db, idesc, (it | kk) != 0);
-          }
-        }
-        umma_commit(&ctl->empty[s]);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_make(1, W_MN, 0, DT, NT);
+    bool ok = true;
+    for (int it = 0; it < cnt; ++it) {
+      const int s = it % C::STAGES;
+      if (!mbar_wait(&ctl->full[s], (it / C::STAGES) & 1, abort)) {
+        ok = false;
+        break;
       }
-      if (ok) umma_commit(&ctl->done);
+      tc_fence_after();
+      const uint32_t w0 = smem_u32(smem + s * C::STAGE);
+      const uint32_t x0 = w0 + DPANEL * (GATED ? 2 : 1);
+#pragma unroll
+      for (int kk = 0; kk < DBK / 16; ++kk) {
+        const uint64_t dx = sdesc_sw128(x0 + kk * 32, 16, 1024);
+#pragma unroll
+        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+          const uint32_t w = w0 + h * DPANEL;
+          const uint64_t dw = W_MN ? sdesc_sw128(w + kk * 2048, DBOX, 1024)
+                                   : sdesc_sw128(w + kk * 32, 16, 1024);
+          umma_bf16(tbase + NT * h, dw, dx, idesc, (it | kk) != 0);
+        }
+      }
+      umma_commit(&ctl->empty[s]);
     }
-  } else {
-    const int q = warp & 3;
-    const int64_t row = m0 + 32 * q + lane;
+    if (ok) umma_commit(&ctl->done);
+  }
+  __syncwarp();
+
+  // ---- this CTA's part of the tile -> shared memory (the ring is free: every
+  // slab has landed and been multiplied)
+  float *part = reinterpret_cast<float *>(smem);
+  {
     const bool ok = mbar_wait(&ctl->done, 0, abort);
     if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();
-      for (int c = 0; c < DT / 32; ++c) {
-        const int64_t col = n0 + 32 * c;
-        if (col >= p.N) break;
-        const int n = static_cast<int>(kq_min<int64_t>(32, p.N - col));
-        const uint32_t ta = tbase + (static_cast<uint32_t>(32 * q) << 16) + 32 * c;
-        float v[32], u[GATED ? 32 : 1];
-        tmem_ld32(ta, v);
-        if constexpr (GATED) tmem_ld32(ta + DT, u);
-        if (row < p.M) finish32<GATED, ACT>(p, row, col, n, v, u);
+      const int feat = 32 * warp + lane;
+#pragma unroll
+      for (int h = 0; h < (GATED ? 2 : 1); ++h) {
+        for (int c = 0; c < NT; c += NT < 32 ? 16 : 32) {
+          constexpr int W = NT < 32 ? 16 : 32;
+          if (t0 + c >= p.M) break;
+          float v[W];
+          const uint32_t ta = tbase + (static_cast<uint32_t>(32 * warp) << 16) + NT * h + c;
+          if constexpr (W == 16) tmem_ld16(ta, v);
+          else tmem_ld32(ta, v);
+#pragma unroll
+          for (int t = 0; t < W; ++t) part[(NT * h + c + t) * DT + feat] = v[t];
+        }
       }
     }
   }
+  tc_fence_before();
+  if (split > 1) cluster_sync_all();
+  else __syncthreads();
+
+  // ---- sum over the parts, epilogue: four features of a token per step
+  const int tokens = static_cast<int>(kq_min<int64_t>(NT, p.M - t0));
+  uint32_t addr[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    addr[r] = split > 1 && r < split ? mapa_shared(smem_u32(part), r) : smem_u32(part);
+  if (!*abort) {
+    for (int e = rank * FTHREADS + threadIdx.x; e < tokens * (DT / 4); e += split * FTHREADS) {
+      const int t = e / (DT / 4), c = e % (DT / 4) * 4;
+      const int64_t col = f0 + c, row = t0 + t;
+      if (col >= p.N) continue;
+      const int n = static_cast<int>(kq_min<int64_t>(4, p.N - col));
+      float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (r < split) {
+          const uint32_t at = addr[r] + static_cast<uint32_t>(t * DT + c) * 4;
+          const float4 x = ld_dsmem_f4(at);
+          v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+          if (GATED) {
+            const float4 y = ld_dsmem_f4(at + NT * DT * 4);
+            u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+          }
+        }
+      }
+      if (!GATED && p.bias) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] += k < n ? __ldg(p.bias + col + k) : 0.f;
+      }
+      if (p.Z) store4(p.Z + row * p.ldz + col, v, n);
+      if (GATED && p.Z) store4(p.Z2 + row * p.ldz + col, u, n);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[k] = act_run(fp.act, v[k]);
+        if (GATED) v[k] *= u[k];
+        else if (p.R) v[k] += k < n ? __bfloat162float(p.R[row * p.ldr + col + k]) : 0.f;
+      }
+      store4(p.Y + row * p.ldy + col, v, n);
+    }
+  }
+  // no CTA leaves while another may still read its part
+  __syncwarp();
+  if (split > 1) cluster_sync_all();
+  else __syncthreads();
 
   // ---- teardown: after an abort make sure no copy or MMA is still in flight
-  tc_fence_before();
-  __syncthreads();
   if (ctl->abort) {
     if (threadIdx.x == 0) report(p.info, KRONQ_ERR_TIMEOUT);
     if (warp == 0 && lane == 0) {
-      const uint64_t t0 = globaltimer();
-      for (int s = 0; s < DSTAGES && s < issued; ++s) {
-        const int last = ((issued - 1 - s) / DSTAGES) * DSTAGES + s;
-        while (!mbar_try_wait(&ctl->full[s], (last / DSTAGES) & 1) &&
-               globaltimer() - t0 < kWaitLimitNs) {
+      const uint64_t c0 = globaltimer();
+      for (int s = 0; s < C::STAGES && s < issued; ++s) {
+        const int last = ((issued - 1 - s) / C::STAGES) * C::STAGES + s;
+        while (!mbar_try_wait(&ctl->full[s], (last / C::STAGES) & 1) &&
+               globaltimer() - c0 < kWaitLimitNs) {
         }
       }
     }
     if (warp == 1 && lane == 0) {
       umma_commit(&ctl->drain);
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(&ctl->drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
+      const uint64_t c0 = globaltimer();
+      while (!mbar_try_wait(&ctl->drain, 0) && globaltimer() - c0 < kWaitLimitNs) {
       }
     }
     __syncthreads();
   }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tbase, COLS);
+    tmem_dealloc(tbase, C::COLS);
   }
 }
 
@@ -579,54 +666,123 @@ kronq_status operand_map(CUtensorMap *m, const void *p, int64_t ld, bool mn, int
             : make_tmap_2d(m, p, true, K, rows, ld, DBK, DT);
 }
 
+// How a product is launched: the few-token kernel splits k over `split` CTAs
+// of a cluster, as many as fit on the chip at once with at least two slabs
+// each.
+template <bool GATED, bool W_MN, int NT>
+kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d, int act) {
+  using C = Few<GATED, NT>;
+  auto *kern = dense_few_kernel<GATED, W_MN, NT>;
+  KQ_TRY(smem_attr(kern, C::SMEM));
+  FewP p;
+  p.d = d;
+  p.act = act;
+  p.tiles_t = static_cast<int>(ceil_div(d.M, NT));
+  const int64_t tiles = p.tiles_t * ceil_div(d.N, DT);
+  int64_t split = kq_min<int64_t>(kq_min<int64_t>(8, 148 * C::PER_SM / tiles),
+                                  d.nk1 * d.nseg / 2);
+  p.split = static_cast<int>(kq_max<int64_t>(split, 1));
+  if (tiles * p.split > 0x7fffffff) return KRONQ_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
+  cfg.blockDim = dim3(FTHREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 1 : 0;
+  KQ_CUDA(cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p));
+  count_launch();
+  return KRONQ_OK;
+}
+
 template <bool GATED, int ACT, bool A_MN, bool B_MN>
-kronq_status launch_dense(cudaStream_t st, const CUtensorMap *tm, DenseP p) {
-  if (p.M > 128) {
-    auto *kern = dense_pair_kernel<GATED, ACT, A_MN, B_MN>;
-    KQ_TRY(smem_attr(kern, PSMEM));
-    p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
-    const int64_t tiles = p.tiles_m * ceil_div(p.N, GATED ? 128 : 256);
-    const int64_t clusters = kq_min<int64_t>(tiles, 74);
-    kern<<<static_cast<unsigned>(2 * clusters), PTHREADS, PSMEM, st>>>(tm[0], tm[1], tm[2], tm[3],
-                                                                       p);
-    KQ_CHECK_LAUNCH();
-    return KRONQ_OK;
-  }
-  auto *kern = dense_kernel<GATED, ACT, A_MN, B_MN>;
-  KQ_TRY(smem_attr(kern, dense_smem<GATED>()));
-  p.tiles_m = static_cast<int>(ceil_div(p.M, DT));
-  const int64_t tiles = p.tiles_m * ceil_div(p.N, DT);
-  if (tiles > 0x7fffffff) return KRONQ_ERR_UNSUPPORTED;
-  kern<<<static_cast<unsigned>(tiles), DTHREADS, dense_smem<GATED>(), st>>>(tm[0], tm[1], tm[2],
-                                                                            tm[3], p);
+kronq_status launch_pair(cudaStream_t st, const CUtensorMap *tm, DenseP p) {
+  auto *kern = dense_pair_kernel<GATED, ACT, A_MN, B_MN>;
+  KQ_TRY(smem_attr(kern, PSMEM));
+  p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
+  const int64_t tiles = p.tiles_m * ceil_div(p.N, GATED ? 128 : 256);
+  const int64_t clusters = kq_min<int64_t>(tiles, 74);
+  kern<<<static_cast<unsigned>(2 * clusters), PTHREADS, PSMEM, st>>>(tm[0], tm[1], tm[2], tm[3],
+                                                                     p);
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
 }
 
-// C = sum over segments of A_s B_s^T (+ R), stored as bf16
-kronq_status product(cudaStream_t st, int64_t M, int64_t N, int64_t K, const Mat &A, bool a_mn,
-                     const Mat &B, const Mat *A2, const Mat *B2, const Mat &R, const Mat &C,
-                     int32_t *info) {
+// Tokens per tile of the few-token kernel, 0 for the pair kernel.
+int few_width(int64_t tokens) {
+  return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 0;
+}
+
+// Tensor maps of D = X W^T by the kernel that takes it: panels of the token
+// operand are NT rows (few) or 128 rows.
+struct Operands {
+  Mat X, W, X2, W2;
+};
+template <bool GATED, bool W_MN>
+kronq_status tokens_product(cudaStream_t st, const Operands &o, const DenseP &p, int act) {
+  const int64_t K = p.K;
+  const int nt = few_width(p.M);
   CUtensorMap tm[4];
   memset(tm, 0, sizeof(tm));
-  KQ_TRY(operand_map(&tm[0], A.p, A.ld, a_mn, M, K));
-  KQ_TRY(operand_map(&tm[1], B.p, B.ld, true, N, K));
-  if (A2) {
-    KQ_TRY(operand_map(&tm[2], A2->p, A2->ld, a_mn, M, K));
-    KQ_TRY(operand_map(&tm[3], B2->p, B2->ld, true, N, K));
+  const uint32_t box = nt ? nt : DT;
+  KQ_TRY(make_tmap_2d(&tm[0], o.X.p, true, K, p.M, o.X.ld, DBK, box));
+  KQ_TRY(operand_map(&tm[1], o.W.p, o.W.ld, W_MN, p.N, K));
+  if (o.X2.p) KQ_TRY(make_tmap_2d(&tm[2], o.X2.p, true, K, p.M, o.X2.ld, DBK, box));
+  if (o.W2.p) KQ_TRY(operand_map(&tm[3], o.W2.p, o.W2.ld, W_MN, p.N, K));
+  switch (nt) {
+    case 16: return launch_few<GATED, W_MN, 16>(st, tm, p, act);
+    case 32: return launch_few<GATED, W_MN, 32>(st, tm, p, act);
+    case 64: return launch_few<GATED, W_MN, 64>(st, tm, p, act);
+    case 128: return launch_few<GATED, W_MN, 128>(st, tm, p, act);
   }
+  if constexpr (W_MN) {
+    return launch_pair<false, KRONQ_ACT_NONE, false, true>(st, tm, p);
+  } else {
+    return with_act(act, [&](auto a) {
+      return launch_pair<GATED, decltype(a)::value, false, false>(st, tm, p);
+    });
+  }
+}
+
+// dX = G W (+ G2 W2) + R
+kronq_status input_grad(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out,
+                        const Operands &o, const Mat &R, const Mat &dX, int32_t *info) {
   DenseP p = {};
-  p.M = M;
-  p.N = N;
-  p.nk1 = static_cast<int>(ceil_div(K, DBK));
-  p.nseg = A2 ? 2 : 1;
+  p.M = n;
+  p.N = d_in;
+  p.K = d_out;
+  p.nk1 = static_cast<int>(ceil_div(d_out, DBK));
+  p.nseg = o.X2.p ? 2 : 1;
   p.R = static_cast<const __nv_bfloat16 *>(R.p);
   p.ldr = R.ld;
-  p.Y = static_cast<__nv_bfloat16 *>(C.p);
-  p.ldy = C.ld;
+  p.Y = static_cast<__nv_bfloat16 *>(dX.p);
+  p.ldy = dX.ld;
   p.info = info;
-  return a_mn ? launch_dense<false, KRONQ_ACT_NONE, true, true>(st, tm, p)
-              : launch_dense<false, KRONQ_ACT_NONE, false, true>(st, tm, p);
+  return tokens_product<false, true>(st, o, p, KRONQ_ACT_NONE);
+}
+
+// dW = G^T X
+kronq_status weight_grad(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out, const Mat &G,
+                         const Mat &X, const Mat &dW, int32_t *info) {
+  CUtensorMap tm[4];
+  memset(tm, 0, sizeof(tm));
+  KQ_TRY(operand_map(&tm[0], G.p, G.ld, true, d_out, n));
+  KQ_TRY(operand_map(&tm[1], X.p, X.ld, true, d_in, n));
+  DenseP p = {};
+  p.M = d_out;
+  p.N = d_in;
+  p.K = n;
+  p.nk1 = static_cast<int>(ceil_div(n, DBK));
+  p.nseg = 1;
+  p.Y = static_cast<__nv_bfloat16 *>(dW.p);
+  p.ldy = dW.ld;
+  p.info = info;
+  return launch_pair<false, KRONQ_ACT_NONE, true, true>(st, tm, p);
 }
 
 kronq_status zero_rows(cudaStream_t st, const Mat &m, int64_t rows, int64_t cols) {
@@ -650,13 +806,10 @@ __nv_bfloat16 *bf(void *p) { return static_cast<__nv_bfloat16 *>(p); }
 kronq_status linear_fwd(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out, const Mat &X,
                         const Mat &W, const float *bias, int act, const Mat &Z, const Mat &R,
                         const Mat &Y, int32_t *info) {
-  CUtensorMap tm[4];
-  memset(tm, 0, sizeof(tm));
-  KQ_TRY(operand_map(&tm[0], X.p, X.ld, false, n, d_in));
-  KQ_TRY(operand_map(&tm[1], W.p, W.ld, false, d_out, d_in));
   DenseP p = {};
   p.M = n;
   p.N = d_out;
+  p.K = d_in;
   p.nk1 = static_cast<int>(ceil_div(d_in, DBK));
   p.nseg = 1;
   p.bias = bias;
@@ -667,22 +820,16 @@ kronq_status linear_fwd(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out,
   p.Y = bf(Y.p);
   p.ldy = Y.ld;
   p.info = info;
-  return with_act(act, [&](auto a) {
-    return launch_dense<false, decltype(a)::value, false, false>(st, tm, p);
-  });
+  return tokens_product<false, false>(st, Operands{X, W, Mat{}, Mat{}}, p, act);
 }
 
 kronq_status gated_fwd(cudaStream_t st, int64_t n, int64_t d, int64_t f, const Mat &X,
                        const Mat &Wg, const Mat &Wu, int act, const Mat &A, const Mat &U,
                        const Mat &H, int32_t *info) {
-  CUtensorMap tm[4];
-  memset(tm, 0, sizeof(tm));
-  KQ_TRY(operand_map(&tm[0], X.p, X.ld, false, n, d));
-  KQ_TRY(operand_map(&tm[1], Wg.p, Wg.ld, false, f, d));
-  KQ_TRY(operand_map(&tm[3], Wu.p, Wu.ld, false, f, d));
   DenseP p = {};
   p.M = n;
   p.N = f;
+  p.K = d;
   p.nk1 = static_cast<int>(ceil_div(d, DBK));
   p.nseg = 1;
   p.Z = bf(A.p);
@@ -691,9 +838,7 @@ kronq_status gated_fwd(cudaStream_t st, int64_t n, int64_t d, int64_t f, const M
   p.Y = bf(H.p);
   p.ldy = H.ld;
   p.info = info;
-  return with_act(act, [&](auto a) {
-    return launch_dense<true, decltype(a)::value, false, false>(st, tm, p);
-  });
+  return tokens_product<true, false>(st, Operands{X, Wg, Mat{}, Wu}, p, act);
 }
 
 kronq_status linear_bwd(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out, const Mat &dY,
@@ -729,9 +874,8 @@ kronq_status linear_bwd(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out,
     G = dZ;
   }
   if (dX.p)
-    KQ_TRY(product(st, n, d_in, d_out, G, false, W, nullptr, nullptr, dXr, dX, info));
-  if (dW.p)
-    KQ_TRY(product(st, d_out, d_in, n, G, true, X, nullptr, nullptr, Mat{}, dW, info));
+    KQ_TRY(input_grad(st, n, d_in, d_out, Operands{G, W, Mat{}, Mat{}}, dXr, dX, info));
+  if (dW.p) KQ_TRY(weight_grad(st, n, d_in, d_out, G, X, dW, info));
   return KRONQ_OK;
 }
 
@@ -756,10 +900,10 @@ kronq_status gated_bwd(cudaStream_t st, int64_t n, int64_t d, int64_t f, const M
   p.G2 = bf(Gu.p);
   p.ldg = Gg.ld;
   KQ_TRY(with_act(act, [&](auto a) { return launch_act_bwd<decltype(a)::value, true>(st, p); }));
-  if (dX.p) KQ_TRY(product(st, n, d, f, Gg, false, Wg, &Gu, &Wu, dXr, dX, info));
+  if (dX.p) KQ_TRY(input_grad(st, n, d, f, Operands{Gg, Wg, Gu, Wu}, dXr, dX, info));
   if (dWg.p) {
-    KQ_TRY(product(st, f, d, n, Gg, true, X, nullptr, nullptr, Mat{}, dWg, info));
-    KQ_TRY(product(st, f, d, n, Gu, true, X, nullptr, nullptr, Mat{}, dWu, info));
+    KQ_TRY(weight_grad(st, n, d, f, Gg, X, dWg, info));
+    KQ_TRY(weight_grad(st, n, d, f, Gu, X, dWu, info));
   }
   return KRONQ_OK;
 }
