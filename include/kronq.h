@@ -506,14 +506,15 @@ kronq_status kronq_gated_bwd(kronq_stream_t stream, const void *dH,
  *   dZ_v = weight tau (q_v - sum over {j: idx_j = v} of p_j)
  * so dZ is the gradient of sum over rows of weight * loss. A place may be
  * named more than once: its p's add up. weight: n fp32, or NULL for all 1. A
- * row of weight 0, or one that keeps no entry, does not count: its logits are
- * not read, and its loss, lse and gradient are 0. Row sums are fp32, the
+ * row of weight 0, or one that keeps no entry, does not count: its logits do
+ * not matter (they may be NaN), and its loss, lse and gradient are 0. Row sums are fp32, the
  * row's logarithms and its loss fp64, rounded once. info_dev: NONFINITE when
  * the loss of a row that counts is not finite.
  * _fwd writes loss and lse (n fp32), _bwd takes that lse and writes dZ (n x
  * vocab, zdtype), _step does both while a row is on the chip. dZ may be Z
  * (the same stride). 1 <= k <= 1024, 1e-4 <= tau <= 1e4, vocab < 2^31;
- * pointers aligned to their element. A row whose logits are all -inf, or that
+ * pointers aligned to their element. Logits of up to 1e32 in magnitude; one
+ * below -1e32 (a mask) counts as -inf. A row whose logits are all -inf, or that
  * holds a NaN or +inf, has lse and gradient NaN.
  */
 kronq_status kronq_distill_fwd(kronq_stream_t stream, const void *Z,

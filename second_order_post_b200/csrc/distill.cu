@@ -4,13 +4,19 @@
 //   loss = tau^2 sum_j p_j (log p_j - z_{I_j} / tau + lse)
 //   dz_v = w tau (q_v - sum_{j: I_j = v} p_j)
 //
-// One CTA a row: the row's maximum, the sum of exponentials, the loss over
-// the k kept entries, then the dense part of the gradient, and last the k
-// places that the teacher names, each written whole (a place named twice gets
-// the same value twice). The exponent z/tau - lse is taken in base 2 as
+// A row's maximum and sum of exponentials, the loss over the k kept entries,
+// the dense part of the gradient, and last the k places that the teacher
+// names, each written whole (a place named twice gets the same value twice).
+// distill_row_kernel keeps a narrow row in registers, distill_wide_kernel a
+// wider one in the shared memory of up to 8 CTAs; rows too wide for that (over
+// 281592 bf16 or 140796 fp32 logits) are read once per pass by distill_kernel. The exponent z/tau - lse is taken in base 2 as
 // z c - L with c = log2(e) / tau and L = lse log2(e); for fp32 logits both
 // constants are held in two parts, so that the exponent is off by half an ulp
 // of itself, not of its larger terms.
+#include <map>
+#include <mutex>
+#include <tuple>
+
 #include "kernels.cuh"
 
 namespace kronq {
@@ -19,6 +25,7 @@ namespace {
 constexpr int DI_THREADS = 512;
 constexpr int DI_WARPS = DI_THREADS / 32;
 constexpr int DI_MAXK = 1024;
+constexpr float NO_LOGIT = -1.0e32f;   // what lies below counts as -inf
 
 struct DistillP {
   const void *Z, *T;
@@ -26,6 +33,7 @@ struct DistillP {
   const int32_t *idx;
   int k, t_bf16;
   float c_hi, c_lo, tau;   // c = log2(e) / tau in two parts
+  double inv_tau;
   const float *weight;
   float *loss, *lse;
   void *dZ;
@@ -133,7 +141,7 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
       s += exp_term<T>(to_f(z[v]), a.c_hi, a.c_lo, b_hi, b_lo);
     s = block_reduce(s, red, 0.f, add);
     lse = double(m) / double(a.tau) + log(double(s));
-    if (m == -INFINITY) lse = double(NAN);
+    if (m < NO_LOGIT) lse = double(NAN);
   } else {
     lse = a.lse[row];
   }
@@ -177,17 +185,676 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
   }
 }
 
+// ---------------------------------------------------------------- narrow rows
+// A CTA of 128 threads a row, eight an SM; the row stays in registers between
+// the sums and the gradient, up to VPT 16-byte vectors a thread, all loaded at
+// once, so the logits are read once and the gradient written once. Each thread
+// makes a pair (maximum m, sum s of exponentials relative to it) of its part
+// and one of its teacher entries; the pairs meet by warp and CTA in a fixed
+// order, scaled to the common maximum. q_v is then exp(z_v / tau - m) / s,
+// without a logarithm; the loss needs one, after the gradient is on its way.
+// Vectors are aligned addresses: the first and last of a row may hold places
+// outside it, which are not read and count as -inf.
+constexpr int VPT = 8;
+
 template <class T>
-kronq_status launch(cudaStream_t st, const DistillP &p, int64_t n, bool fwd, bool bwd) {
+struct VecOf {
+  static constexpr int E = 16 / sizeof(T);
+};
+
+template <class T>
+__device__ __forceinline__ void unpack(const uint4 &r, float *v) {
+  if constexpr (sizeof(T) == 4) {
+    v[0] = __uint_as_float(r.x);
+    v[1] = __uint_as_float(r.y);
+    v[2] = __uint_as_float(r.z);
+    v[3] = __uint_as_float(r.w);
+  } else {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      v[2 * t] = __uint_as_float(w[t] << 16);
+      v[2 * t + 1] = __uint_as_float(w[t] & 0xffff0000u);
+    }
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void store_vec(T *p, const float *v) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    uint4 o;
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&o);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) h[t] = __floats2bfloat162_rn(v[2 * t], v[2 * t + 1]);
+    *reinterpret_cast<uint4 *>(p) = o;
+  }
+}
+
+__device__ __forceinline__ float ex2(float a) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a));
+  return e;
+}
+
+// 2^((z - m) c): the difference first, so that its rounding is relative to it
+template <class T>
+__device__ __forceinline__ float exp_rel(float z, float m, float c_hi, float c_lo) {
+  if constexpr (sizeof(T) == 4) {
+    const float d = max_nan(z - m, -1.0e30f);
+    return ex2(fmaf(d, c_hi, d * c_lo));
+  } else {
+    return ex2((z - m) * c_hi);
+  }
+}
+
+// (m, s) pairs: m may be -inf (then s is 0)
+__device__ __forceinline__ float rescale(float s, float from, float to, float c) {
+  return from == -INFINITY ? 0.f : s * ex2((from - to) * c);
+}
+
+// largest value of a warp, NaN if one is
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// (m, s) over a warp, scaled to the common maximum
+__device__ __forceinline__ void warp_pair(float &m, float &s, float c) {
+  const float wm = warp_max_nan(m);
+  s = warp_sum(rescale(s, m, wm, c));
+  m = wm;
+}
+
+template <class T, bool FWD, bool BWD, int THREADS>
+__global__ void __launch_bounds__(THREADS, 8)
+    distill_row_kernel(const DistillP a) {
+  constexpr int E = VecOf<T>::E, WARPS = THREADS / 32;
+  __shared__ __align__(16) float p_s[DI_MAXK], z_s[DI_MAXK];
+  __shared__ __align__(16) int32_t i_s[DI_MAXK];
+  __shared__ __align__(16) float4 wpair[WARPS];   // (m, s) of the row, (m, s) of the teacher
+  __shared__ double loss_s[WARPS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t row = blockIdx.x;
+  const int vocab = static_cast<int>(a.vocab);
+  const T *z = static_cast<const T *>(a.Z) + row * a.ldz;
+  T *dz = static_cast<T *>(a.dZ) + row * a.lddz;
+  const float w = a.weight ? a.weight[row] : 1.f;
+  const bool live = w != 0.f;
+  const int head = static_cast<int>(reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
+  const int nvec = (vocab + head + E - 1) / E;
+  const float c2e = a.c_hi;                                 // log2(e) / tau
+
+  uint4 raw[VPT];
+  float tm = -INFINITY, ts = 0.f;     // the teacher's (m, s)
+  if (live) {
+    // ---- the teacher's entries, one a thread (k <= THREADS: no loop)
+    for (int j = tid; j < a.k; j += THREADS) {
+      i_s[j] = a.idx[row * a.ldt + j];
+      p_s[j] = a.t_bf16
+                   ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.T)[row * a.ldt + j])
+                   : static_cast<const float *>(a.T)[row * a.ldt + j];
+    }
+    // ---- the row's vectors, all in flight at once
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * THREADS + tid, e = v * E - head;
+      constexpr uint32_t NINF = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+      raw[i] = make_uint4(NINF, NINF, NINF, NINF);
+      if (v >= nvec) continue;
+      if (e >= 0 && e + E <= vocab) {
+        raw[i] = *reinterpret_cast<const uint4 *>(z + e);
+      } else {
+        uint32_t *r = reinterpret_cast<uint32_t *>(&raw[i]);
+#pragma unroll
+        for (int t = 0; t < E; ++t) {
+          if (e + t < 0 || e + t >= vocab) continue;
+          if constexpr (sizeof(T) == 4) {
+            r[t] = __float_as_uint(z[e + t]);
+          } else {
+            const uint32_t b = __bfloat16_as_ushort(z[e + t]);
+            r[t / 2] = t % 2 ? (r[t / 2] & 0xffffu) | b << 16 : (r[t / 2] & 0xffff0000u) | b;
+          }
+        }
+      }
+    }
+    for (int j = tid; j < a.k; j += THREADS) {
+      const int i = i_s[j];
+      const bool in = i >= 0 && i < vocab;
+      if (i >= vocab) report(a.info, KRONQ_ERR_INVALID_ARG);
+      const float t = in ? p_s[j] : -INFINITY;
+      z_s[j] = in ? to_f(z[i]) : 0.f;
+      i_s[j] = t != -INFINITY ? i : -1;
+      p_s[j] = t;
+      const float m2 = max_nan(tm, t);
+      ts = rescale(ts, tm, m2, c2e) + (t == -INFINITY ? 0.f : ex2((t - m2) * c2e));
+      tm = m2;
+    }
+  }
+  // ---- (m, s) of the row
+  float m = -INFINITY, s = 0.f;
+  if (live) {
+    if (FWD) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float v[E];
+        unpack<T>(raw[i], v);
+#pragma unroll
+        for (int t = 0; t < E; ++t) m = max_nan(m, v[t]);
+      }
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      if (m != -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          float v[E];
+          unpack<T>(raw[i], v);
+#pragma unroll
+          for (int t = 0; t < E; ++t) acc[t % 4] += exp_rel<T>(v[t], m, a.c_hi, a.c_lo);
+        }
+      }
+      s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      warp_pair(m, s, c2e);
+    }
+    warp_pair(tm, ts, c2e);
+    if (lane == 0) wpair[warp] = make_float4(m, s, tm, ts);
+  }
+  __syncthreads();
+  if (live) {
+    m = tm = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      const float4 x = wpair[k];
+      m = max_nan(m, x.x);
+      tm = max_nan(tm, x.z);
+    }
+    s = ts = 0.f;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      const float4 x = wpair[k];
+      if (FWD) s += rescale(x.y, x.x, m, c2e);
+      ts += rescale(x.w, x.z, tm, c2e);
+    }
+  }
+  const bool counts = live && tm != -INFINITY;   // some entry is kept
+  if (FWD) {
+    if (m < NO_LOGIT) m = NAN;   // no logit at all: q has no value
+  }
+  // ---- gradient
+  const float wt = w * a.tau;
+  float b_hi = 0.f, b_lo = 0.f, scale = wt;
+  if (BWD) {
+    if (FWD) {            // 2^(z c - m c) / s
+      b_hi = m * a.c_hi;
+      b_lo = fmaf(m, a.c_hi, -b_hi) + m * a.c_lo;
+      scale = __fdiv_rn(wt, s);
+    } else {              // 2^(z c - lse log2 e)
+      constexpr float L2E_HI = 1.44269502f, L2E_LO = 1.92596299e-8f;
+      const float lse = a.lse[row];
+      b_hi = lse * L2E_HI;
+      b_lo = fmaf(lse, L2E_HI, -b_hi) + lse * L2E_LO;
+    }
+    const bool vec = (reinterpret_cast<uintptr_t>(dz) & 15) == (reinterpret_cast<uintptr_t>(z) & 15);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * THREADS + tid, e = v * E - head;
+      if (v >= nvec) continue;
+      float g[E];
+      if (counts) {
+        unpack<T>(raw[i], g);
+#pragma unroll
+        for (int t = 0; t < E; ++t)
+          g[t] = scale * exp_term<T>(g[t], a.c_hi, a.c_lo, b_hi, b_lo);
+      } else {
+#pragma unroll
+        for (int t = 0; t < E; ++t) g[t] = 0.f;
+      }
+      if (vec && e >= 0 && e + E <= vocab) {
+        store_vec(dz + e, g);
+      } else {
+#pragma unroll
+        for (int t = 0; t < E; ++t)
+          if (e + t >= 0 && e + t < vocab) put(dz + e + t, g[t]);
+      }
+    }
+  }
+  // ---- loss; p_s becomes p
+  double loss = 0.0;
+  if (counts) {
+    for (int j = tid; j < a.k; j += THREADS) {
+      const float t = p_s[j];
+      const float p = i_s[j] >= 0 ? __fdiv_rn(ex2((t - tm) * c2e), ts) : 0.f;
+      p_s[j] = p;
+      if (FWD && p != 0.f)
+        loss += double(p) * ((double(t) - double(tm) - double(z_s[j]) + double(m)) * a.inv_tau +
+                             log(double(s) / double(ts)));
+    }
+    if (FWD && warp * 32 < a.k) {
+      loss = warp_sum_d(loss);
+      if (lane == 0) loss_s[warp] = loss;
+    }
+  }
+  __syncthreads();
+  if (FWD && tid == 0) {
+    float l = 0.f, lse = 0.f;
+    if (counts) {
+      for (int k = 1; k < WARPS && k * 32 < a.k; ++k) loss += loss_s[k];
+      l = float(double(a.tau) * double(a.tau) * loss);
+      lse = float(double(m) * a.inv_tau + log(double(s)));
+      if (!isfinite(l)) report(a.info, KRONQ_ERR_NONFINITE);
+    }
+    a.loss[row] = l;
+    if (a.lse) a.lse[row] = lse;
+  }
+  if (BWD && counts) {   // the places the teacher names
+    for (int j = tid; j < a.k; j += THREADS) {
+      const int i = i_s[j];
+      if (i < 0) continue;
+      float p = 0.f;
+      for (int l = 0; l < a.k; ++l) p += i_s[l] == i ? p_s[l] : 0.f;
+      put(dz + i, scale * exp_term<T>(z_s[j], a.c_hi, a.c_lo, b_hi, b_lo) - wt * p);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- wide rows
+// For rows that take a CTA or several: a row lies over `parts` CTAs (with the
+// forward pass a cluster), each with its part in shared memory, where a bulk
+// copy brings it. The part is read there three times: maximum, sum of
+// exponentials, gradient. The CTAs are persistent and independent, several an
+// SM, so that the copies of some run under the arithmetic of others; while a
+// CTA's own copy is on its way it collects the teacher's entries of that row
+// and writes the rest of the row before (the places that the teacher names,
+// the loss).
+//   The copy takes whole 16-byte vectors inside the row; the threads that own
+// the row's first and last vector put those together when they are cut.
+//   Measured (4096 rows of 32000 bf16 logits, k = 64, gradient too): 107 us =
+// 4.9 TB/s with three CTAs an SM of 384 threads; two of 512 threads 120 us, six
+// of 192 threads on half rows (clusters of two) 121 us; a row kept in registers
+// and one CTA of 512 threads an SM 135 us (its phases do not overlap).
+constexpr int ST = 384;
+constexpr int WIDE_VEC = 4400;   // vectors of a part: 70 KB, three CTAs an SM
+
+// ln(x) for a normal x > 0, off by less than 4e-8: exponent times ln 2 in
+// fp64, plus the fp32 logarithm of a mantissa in [0.75, 1.5)
+__device__ __forceinline__ double log_split(float x) {
+  const int ex = (__float_as_int(x) - 0x3f400000) >> 23;
+  const float f = __int_as_float(__float_as_int(x) - (ex << 23));
+  return double(ex) * 0.69314718055994530942 + double(logf(f));
+}
+
+// largest of 8 bf16 or 4 fp32
+template <class T>
+__device__ __forceinline__ float max_vec(const uint4 &r) {
+  if constexpr (sizeof(T) == 4) {
+    return max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)),
+                   max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
+  } else {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r);
+    const __nv_bfloat162 x = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    return max_nan(__low2float(x), __high2float(x));
+  }
+}
+
+template <class T>
+__device__ __forceinline__ uint4 neg_inf_vec() {
+  constexpr uint32_t b = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+  return make_uint4(b, b, b, b);
+}
+
+// The vector at element e of a row of `vocab`, places outside it -inf.
+template <class T>
+__device__ __forceinline__ uint4 cut_vec(const T *z, int e, int vocab) {
+  constexpr int E = VecOf<T>::E;
+  uint4 o = neg_inf_vec<T>();
+  uint32_t *r = reinterpret_cast<uint32_t *>(&o);
+#pragma unroll
+  for (int t = 0; t < E; ++t) {
+    if (e + t < 0 || e + t >= vocab) continue;
+    if constexpr (sizeof(T) == 4) {
+      r[t] = __float_as_uint(z[e + t]);
+    } else {
+      const uint32_t b = __bfloat16_as_ushort(z[e + t]);
+      r[t / 2] = t % 2 ? (r[t / 2] & 0xffffu) | b << 16 : (r[t / 2] & 0xffff0000u) | b;
+    }
+  }
+  return o;
+}
+
+template <class T, bool FWD, bool BWD>
+__global__ void __launch_bounds__(ST, 3)
+    distill_wide_kernel(const DistillP a, int parts, int per, int kp, int n) {
+  constexpr int E = VecOf<T>::E, WARPS = ST / 32;
+  extern __shared__ __align__(128) uint8_t dsm[];
+  uint4 *buf = reinterpret_cast<uint4 *>(dsm);
+  float *t_s = reinterpret_cast<float *>(buf + per);                  // [2][kp]: T, then w tau p
+  int32_t *i_s = reinterpret_cast<int32_t *>(t_s + 2 * kp);           // [2][kp]: places
+  float *z_s = reinterpret_cast<float *>(i_s + 2 * kp);               // [2][kp]: z, then w tau q
+  __shared__ __align__(16) float4 wpair[32];         // (m, s) of the row, of the teacher
+  __shared__ __align__(16) float4 pair[2];           // the CTA's (m, s)
+  __shared__ double loss_s[WARPS];
+  __shared__ uint64_t bar;
+  __shared__ int abort_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool clus = FWD && parts > 1;
+  const int rank = blockIdx.x % parts, vocab = static_cast<int>(a.vocab), k = a.k;
+  const int stride = gridDim.x / parts;
+  const float c2e = a.c_hi;
+  if (tid == 0) {
+    mbar_init(&bar, 1);
+    abort_s = 0;
+    fence_mbar_init();
+  }
+  if (tid < 32) wpair[tid] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+  for (int j = tid; j < 2 * kp; j += ST) i_s[j] = -1, t_s[j] = 0.f;
+  __syncthreads();
+
+  // where this CTA's part of a row lies: `cnt` vectors from element e0 (which
+  // may be negative: the row's first vector is an aligned address)
+  auto row_ptr = [&](int r) { return static_cast<const T *>(a.Z) + int64_t(r) * a.ldz; };
+  auto part_of = [&](const T *z, int &e0, int &cnt) {
+    const int head = static_cast<int>(reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
+    const int nvec = (vocab + head + E - 1) / E, v0 = per * rank;
+    e0 = v0 * E - head;
+    cnt = kq_max(kq_min(nvec - v0, per), 0);
+  };
+  // Starts the copy of a row's part (all threads call it, the buffer is free):
+  // whole vectors by bulk copy, cut ones by their owners. A part without a
+  // whole vector completes the barrier's phase all the same.
+  uint32_t copies = 0;
+  auto fetch = [&](int r) {
+    const T *z = row_ptr(r);
+    int e0, cnt;
+    part_of(z, e0, cnt);
+    const int lo = e0 < 0 ? 1 : 0;
+    const bool cut = cnt > 0 && e0 + cnt * E > vocab;
+    const int hi = cut ? cnt - 1 : cnt;
+    if (tid == 0) {
+      const uint32_t bytes = hi > lo ? (hi - lo) * 16u : 0u;
+      mbar_expect_tx(&bar, bytes);
+      if (bytes) bulk_load(buf + lo, z + (e0 + lo * E), bytes, &bar);
+      if (lo && cnt > 0) buf[0] = cut_vec(z, e0, vocab);
+    }
+    if (cut && tid == (cnt - 1) % ST) buf[cnt - 1] = cut_vec(z, e0 + (cnt - 1) * E, vocab);
+    if (lo || cut) fence_proxy_async_smem();   // a later copy may write there
+    ++copies;
+  };
+  auto weight_of = [&](int64_t r) { return r >= n ? 0.f : a.weight ? a.weight[r] : 1.f; };
+
+  int row = blockIdx.x / parts;
+  float w = weight_of(row);
+  if (w != 0.f) fetch(row);
+  uint32_t phase = 0;
+  int par = 0;
+  bool abort = false;       // a wait ran out: no more copies, the barriers go on
+  for (; row < n; par ^= 1) {
+    const bool live = w != 0.f;
+    const float w1 = weight_of(int64_t(row) + stride);
+    const float lse_in = !FWD && live ? a.lse[row] : 0.f;
+    const T *z = row_ptr(row);
+    float *tr = t_s + par * kp, *zr = z_s + par * kp;
+    int32_t *ir = i_s + par * kp;
+    // ---- the teacher's entries, while the row is on its way
+    float tm = -INFINITY, ts = 0.f;
+    if (live) {
+      for (int j = tid; j < k; j += ST) {
+        const int64_t at = row * a.ldt + j;
+        int i = a.idx[at];
+        float t = a.t_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.T)[at])
+                           : static_cast<const float *>(a.T)[at];
+        if (i >= vocab) report(a.info, KRONQ_ERR_INVALID_ARG);
+        if (i < 0 || i >= vocab) t = -INFINITY;
+        if (t == -INFINITY) i = -1;
+        zr[j] = i >= 0 ? to_f(z[i]) : 0.f;
+        tr[j] = t;
+        ir[j] = i;
+        const float m2 = max_nan(tm, t);
+        ts = rescale(ts, tm, m2, c2e) + (i < 0 ? 0.f : ex2((t - m2) * c2e));
+        tm = m2;
+      }
+      if (warp * 32 < k) warp_pair(tm, ts, c2e);
+    }
+    // ---- (m, s) of this part
+    int e0, cnt;
+    part_of(z, e0, cnt);
+    float m = -INFINITY, s = 0.f;
+    if (live) {
+      if (!mbar_wait(&bar, phase, &abort_s)) abort = true;
+      phase ^= 1;
+      if (FWD) {
+#pragma unroll 4
+        for (int v = tid; v < cnt; v += ST) m = max_nan(m, max_vec<T>(buf[v]));
+        m = m < NO_LOGIT ? NO_LOGIT : m;    // exponents of masked logits: -inf
+        const float mc = m * a.c_hi;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int v = tid; v < cnt; v += ST) {
+          float x[E];
+          unpack<T>(buf[v], x);
+#pragma unroll
+          for (int t = 0; t < E; ++t)
+            acc[t % 4] += sizeof(T) == 4 ? exp_rel<T>(x[t], m, a.c_hi, a.c_lo)
+                                         : ex2(fmaf(x[t], a.c_hi, -mc));
+        }
+        s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        // bf16: the exponentials are relative to mc as rounded
+        if (sizeof(T) == 2) s = fmaf(s, -0.69314718f * fmaf(m, a.c_hi, -mc), s);
+        warp_pair(m, s, c2e);
+      }
+    }
+    if (lane == 0) wpair[warp] = make_float4(m, s, tm, ts);
+    __syncthreads();
+    if (!BWD && w1 != 0.f && !abort) fetch(row + stride);   // the buffer is free
+    {
+      const float4 x = wpair[lane];
+      m = FWD ? warp_max_nan(x.x) : 0.f;
+      tm = warp_max_nan(x.z);
+      s = FWD ? warp_sum(rescale(x.y, x.x, m, c2e)) : 0.f;
+      ts = warp_sum(rescale(x.w, x.z, tm, c2e));
+    }
+    const bool counts = live && tm != -INFINITY;   // some entry is kept
+    if (clus) {
+      if (tid == 0) pair[par] = make_float4(m, s, 0.f, 0.f);
+      __syncwarp();
+      cluster_sync_all();
+      const float4 x = lane < parts ? ld_dsmem_f4(mapa_shared(smem_u32(&pair[par]), lane))
+                                    : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      m = warp_max_nan(x.x);
+      s = warp_sum(rescale(x.y, x.x, m, c2e));
+    }
+    if (FWD && m <= NO_LOGIT) m = NAN;   // no logit at all: q has no value
+    // ---- the dense gradient
+    const float wt = w * a.tau;
+    float b_hi = 0.f, b_lo = 0.f, scale = wt;
+    if (BWD) {
+      if (FWD) {            // 2^(z c - m c) / s
+        b_hi = m * a.c_hi;
+        b_lo = fmaf(m, a.c_hi, -b_hi) + m * a.c_lo;
+        scale = __fdiv_rn(wt, s);
+      } else {              // 2^(z c - lse log2 e)
+        constexpr float L2E_HI = 1.44269502f, L2E_LO = 1.92596299e-8f;
+        b_hi = lse_in * L2E_HI;
+        b_lo = fmaf(lse_in, L2E_HI, -b_hi) + lse_in * L2E_LO;
+      }
+      // bf16: the exponent's second part is the same for the whole row
+      if (sizeof(T) == 2) scale = fmaf(scale, -0.69314718f * b_lo, scale);
+      T *dz = static_cast<T *>(a.dZ) + int64_t(row) * a.lddz;
+      const bool vec =
+          (reinterpret_cast<uintptr_t>(dz) & 15) == (reinterpret_cast<uintptr_t>(z) & 15);
+#pragma unroll 2
+      for (int v = tid; v < cnt; v += ST) {
+        const int at = e0 + v * E;
+        float g[E];
+        unpack<T>(buf[v], g);
+#pragma unroll
+        for (int t = 0; t < E; ++t)
+          g[t] = counts ? scale * exp_term<T>(g[t], a.c_hi, a.c_lo, b_hi, b_lo) : 0.f;
+        if (vec && at >= 0 && at + E <= vocab) {
+          store_vec(dz + at, g);
+        } else {
+          for (int t = 0; t < E; ++t)
+            if (at + t >= 0 && at + t < vocab) put(dz + at + t, g[t]);
+        }
+      }
+    }
+    // ---- the teacher's p (kept as w tau p) and its part of the loss
+    if (counts) {
+      const float rts = __fdiv_rn(1.f, ts);
+      double loss = 0.0;
+      for (int j = tid; j < k; j += ST) {
+        const float t = tr[j], zj = zr[j];
+        const float p = ir[j] >= 0 ? ex2((t - tm) * c2e) * rts : 0.f;
+        if (FWD && rank == 0 && p != 0.f)
+          loss += double(p) * ((double(t) - double(tm) - double(zj) + double(m)) * a.inv_tau);
+        if (BWD) {
+          tr[j] = wt * p;
+          zr[j] = scale * exp_term<T>(zj, a.c_hi, a.c_lo, b_hi, b_lo);
+        }
+      }
+      if (FWD && rank == 0 && warp * 32 < k) {
+        loss = warp_sum_d(loss);
+        if (lane == 0) loss_s[warp] = loss;
+      }
+    }
+    __syncthreads();
+    if (BWD && w1 != 0.f && !abort) fetch(row + stride);   // the buffer is free
+    // ---- the places the teacher names in this part, behind the dense stores:
+    // w tau (q - the sum of the p of all entries that name the place)
+    if (BWD && counts) {
+      T *dz = static_cast<T *>(a.dZ) + int64_t(row) * a.lddz;
+      const int4 *pl = reinterpret_cast<const int4 *>(ir);
+      const float4 *pp = reinterpret_cast<const float4 *>(tr);
+      for (int j = tid; j < k; j += ST) {
+        const int i = ir[j];
+        if (i < 0 || i < e0 || i >= e0 + cnt * E) continue;
+        float p = 0.f;
+#pragma unroll 4
+        for (int l = 0; l < kp / 4; ++l) {
+          const int4 x = pl[l];
+          const float4 y = pp[l];
+          p += x.x == i ? y.x : 0.f;
+          p += x.y == i ? y.y : 0.f;
+          p += x.z == i ? y.z : 0.f;
+          p += x.w == i ? y.w : 0.f;
+        }
+        put(dz + i, zr[j] - p);
+      }
+    }
+    if (FWD && rank == 0 && tid == ST - 1) {
+      float l = 0.f, lse = 0.f;
+      if (counts) {
+        double sum = 0.0;
+        for (int x = 0; x < WARPS && x * 32 < k; ++x) sum += loss_s[x];
+        const double ls = log_split(s);
+        l = float(double(a.tau) * double(a.tau) * (sum + (ls - log_split(ts))));
+        lse = float(double(m) * a.inv_tau + ls);
+        if (!isfinite(l)) report(a.info, KRONQ_ERR_NONFINITE);
+      }
+      a.loss[row] = l;
+      if (a.lse) a.lse[row] = lse;
+    }
+    w = w1;
+    if (stride >= n - row) break;
+    row += stride;
+  }
+  if (abort) {   // a copy may still be in flight
+    if (tid == 0) report(a.info, KRONQ_ERR_TIMEOUT);
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(&bar, (copies & 1) ^ 1) && globaltimer() - t0 < kWaitLimitNs) {
+    }
+  }
+  __syncwarp();
+  // no CTA leaves while another may still read its pair
+  if (clus) cluster_sync_all();
+}
+
+// How many rows (clusters of `parts` CTAs) are on the chip at once; asked once
+// per kernel, device and size.
+kronq_status resident_rows(const void *kern, int threads, int smem, int parts, bool clus,
+                           int *rows) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, const void *, int, int>, int> known;
+  int dev = 0;
+  KQ_CUDA(cudaGetDevice(&dev));
+  std::lock_guard<std::mutex> lock(mu);
+  int &v = known[std::make_tuple(dev, kern, smem, parts)];
+  if (v == 0) {
+    int got = 0;
+    if (clus) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(parts));
+      cfg.blockDim = dim3(threads);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      KQ_CUDA(cudaOccupancyMaxActiveClusters(&got, kern, &cfg));
+    } else {
+      int sms = 0;
+      KQ_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+      KQ_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&got, kern, threads, smem));
+      got = got * sms / parts;
+    }
+    v = kq_max(got, 1);
+  }
+  *rows = v;
+  return KRONQ_OK;
+}
+
+template <class T, bool FWD, bool BWD>
+kronq_status launch_wide(cudaStream_t st, const DistillP &p, int64_t n, int64_t nvec, int parts) {
+  auto *kern = distill_wide_kernel<T, FWD, BWD>;
+  const int per = static_cast<int>(ceil_div(nvec, parts)), kp = (p.k + 3) / 4 * 4;
+  const bool clus = FWD && parts > 1;
+  const int smem = (per * 16 + 24 * kp + 1023) / 1024 * 1024;
+  KQ_TRY(smem_attr(kern, smem));
+  int rows = 0;
+  KQ_TRY(resident_rows(reinterpret_cast<const void *>(kern), ST, smem, parts, clus, &rows));
+  rows = static_cast<int>(kq_min<int64_t>(n, rows));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows * parts));
+  cfg.blockDim = dim3(ST);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = clus ? 1 : 0;
+  KQ_CUDA(cudaLaunchKernelEx(&cfg, kern, p, parts, per, kp, static_cast<int>(n)));
+  count_launch();
+  return KRONQ_OK;
+}
+
+template <class T, bool FWD, bool BWD>
+kronq_status launch_mode(cudaStream_t st, const DistillP &p, int64_t n) {
+  // a row that starts off a 16-byte boundary touches one vector more
+  const int64_t nvec = ceil_div(p.vocab, VecOf<T>::E) + 1;
   const unsigned grid = static_cast<unsigned>(n);
-  if (fwd && bwd)
-    distill_kernel<T, true, true><<<grid, DI_THREADS, 0, st>>>(p);
-  else if (fwd)
-    distill_kernel<T, true, false><<<grid, DI_THREADS, 0, st>>>(p);
-  else
-    distill_kernel<T, false, true><<<grid, DI_THREADS, 0, st>>>(p);
+  if (nvec <= 128 * VPT) {
+    distill_row_kernel<T, FWD, BWD, 128><<<grid, 128, 0, st>>>(p);
+    KQ_CHECK_LAUNCH();
+    return KRONQ_OK;
+  }
+  const int64_t parts = ceil_div(nvec, WIDE_VEC);
+  if (parts <= 8) return launch_wide<T, FWD, BWD>(st, p, n, nvec, static_cast<int>(parts));
+  distill_kernel<T, FWD, BWD><<<grid, DI_THREADS, 0, st>>>(p);
   KQ_CHECK_LAUNCH();
   return KRONQ_OK;
+}
+
+template <class T>
+kronq_status launch(cudaStream_t st, const DistillP &p, int64_t n, bool fwd, bool bwd) {
+  return fwd && bwd ? launch_mode<T, true, true>(st, p, n)
+         : fwd      ? launch_mode<T, true, false>(st, p, n)
+                    : launch_mode<T, false, true>(st, p, n);
 }
 
 }  // namespace
@@ -208,6 +875,7 @@ kronq_status distill(cudaStream_t st, const DistillArgs &a) {
   p.c_hi = float(c);
   p.c_lo = float(c - double(p.c_hi));
   p.tau = a.tau;
+  p.inv_tau = 1.0 / double(a.tau);
   p.weight = a.weight;
   p.loss = a.loss;
   p.lse = a.lse;
