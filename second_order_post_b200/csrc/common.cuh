@@ -85,7 +85,50 @@ constexpr uint64_t kWaitLimitNs = 4000000000ull;
 // Upper bound of the wait limit kronq_selftest_timeout accepts.
 constexpr uint64_t kSelftestMaxNs = 1000000000ull;
 
+// Launches a kernel in clusters of `cluster` CTAs (1: none). `early`: the
+// kernel may start while the kernel before it on the stream still runs; it has
+// to call pdl_wait() before it touches global memory.
+template <class... P, class... A>
+inline kronq_status launch_kernel(cudaStream_t st, void (*kern)(P...), int64_t grid, int threads,
+                                  size_t smem, int cluster, bool early, A... args) {
+  if (grid > 0x7fffffff) return KRONQ_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  if (early) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  KQ_CUDA(cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...));
+  count_launch();
+  return KRONQ_OK;
+}
+
 // ----------------------------------------------------------------- device side
+// Waits until the kernels before this one on the stream have completed and
+// their writes are visible (at once if the kernel was not launched early).
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// From here on the next kernel on the stream may start (it waits for this one
+// in pdl_wait). Call it when this CTA holds all it needs (tensor memory): the
+// next kernel's CTAs take what is left.
+__device__ __forceinline__ void pdl_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

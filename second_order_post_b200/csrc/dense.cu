@@ -187,11 +187,17 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
     tmem_alloc(&ctl->tmem_base, C::COLS);
     tmem_relinquish();
   }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmX);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = ctl->tmem_base;
   volatile int *abort = &ctl->abort;
+  pdl_launch();
+  pdl_wait();
 
   int issued = 0;
   if (warp == 0 && lane == 0) {
@@ -388,7 +394,7 @@ __device__ __forceinline__ void pair_tile(int64_t t, int tiles_m, int tiles_n, i
 }
 
 template <bool GATED, int ACT, bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
+__global__ void __launch_bounds__(PTHREADS, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmA2,
@@ -427,6 +433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PTHREADS, 1)
   tc_fence_after();
   const uint32_t tbase = ctl->tmem_base;
   volatile int *abort = &ctl->abort;
+  pdl_launch();
+  pdl_wait();
 
   int64_t issued = 0;
   if (warp == 8) {
@@ -682,22 +690,8 @@ kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d,
   int64_t split = kq_min<int64_t>(kq_min<int64_t>(8, 148 * C::PER_SM / tiles),
                                   d.nk1 * d.nseg / 2);
   p.split = static_cast<int>(kq_max<int64_t>(split, 1));
-  if (tiles * p.split > 0x7fffffff) return KRONQ_ERR_UNSUPPORTED;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
-  cfg.blockDim = dim3(FTHREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.split > 1 ? 1 : 0;
-  KQ_CUDA(cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], p));
-  count_launch();
-  return KRONQ_OK;
+  return launch_kernel(st, kern, tiles * p.split, FTHREADS, C::SMEM, p.split, true, tm[0], tm[1],
+                       tm[2], tm[3], p);
 }
 
 template <bool GATED, int ACT, bool A_MN, bool B_MN>
@@ -707,10 +701,8 @@ kronq_status launch_pair(cudaStream_t st, const CUtensorMap *tm, DenseP p) {
   p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
   const int64_t tiles = p.tiles_m * ceil_div(p.N, GATED ? 128 : 256);
   const int64_t clusters = kq_min<int64_t>(tiles, 74);
-  kern<<<static_cast<unsigned>(2 * clusters), PTHREADS, PSMEM, st>>>(tm[0], tm[1], tm[2], tm[3],
-                                                                     p);
-  KQ_CHECK_LAUNCH();
-  return KRONQ_OK;
+  return launch_kernel(st, kern, 2 * clusters, PTHREADS, PSMEM, 2, true, tm[0], tm[1], tm[2],
+                       tm[3], p);
 }
 
 // Tokens per tile of the few-token kernel, 0 for the pair kernel.

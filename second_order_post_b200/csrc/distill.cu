@@ -281,6 +281,8 @@ __global__ void __launch_bounds__(THREADS, 8)
   const int vocab = static_cast<int>(a.vocab);
   const T *z = static_cast<const T *>(a.Z) + row * a.ldz;
   T *dz = static_cast<T *>(a.dZ) + row * a.lddz;
+  pdl_launch();
+  pdl_wait();
   const float w = a.weight ? a.weight[row] : 1.f;
   const bool live = w != 0.f;
   const int head = static_cast<int>(reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
@@ -549,6 +551,8 @@ __global__ void __launch_bounds__(ST, 3)
   if (tid < 32) wpair[tid] = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
   for (int j = tid; j < 2 * kp; j += ST) i_s[j] = -1, t_s[j] = 0.f;
   __syncthreads();
+  pdl_launch();
+  pdl_wait();
 
   // where this CTA's part of a row lies: `cnt` vectors from element e0 (which
   // may be negative: the row's first vector is an aligned address)
@@ -816,38 +820,19 @@ kronq_status launch_wide(cudaStream_t st, const DistillP &p, int64_t n, int64_t 
   int rows = 0;
   KQ_TRY(resident_rows(reinterpret_cast<const void *>(kern), ST, smem, parts, clus, &rows));
   rows = static_cast<int>(kq_min<int64_t>(n, rows));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows * parts));
-  cfg.blockDim = dim3(ST);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = clus ? 1 : 0;
-  KQ_CUDA(cudaLaunchKernelEx(&cfg, kern, p, parts, per, kp, static_cast<int>(n)));
-  count_launch();
-  return KRONQ_OK;
+  return launch_kernel(st, kern, int64_t(rows) * parts, ST, smem, clus ? parts : 1, true, p, parts,
+                       per, kp, static_cast<int>(n));
 }
 
 template <class T, bool FWD, bool BWD>
 kronq_status launch_mode(cudaStream_t st, const DistillP &p, int64_t n) {
   // a row that starts off a 16-byte boundary touches one vector more
   const int64_t nvec = ceil_div(p.vocab, VecOf<T>::E) + 1;
-  const unsigned grid = static_cast<unsigned>(n);
-  if (nvec <= 128 * VPT) {
-    distill_row_kernel<T, FWD, BWD, 128><<<grid, 128, 0, st>>>(p);
-    KQ_CHECK_LAUNCH();
-    return KRONQ_OK;
-  }
+  if (nvec <= 128 * VPT)
+    return launch_kernel(st, distill_row_kernel<T, FWD, BWD, 128>, n, 128, 0, 1, true, p);
   const int64_t parts = ceil_div(nvec, WIDE_VEC);
   if (parts <= 8) return launch_wide<T, FWD, BWD>(st, p, n, nvec, static_cast<int>(parts));
-  distill_kernel<T, FWD, BWD><<<grid, DI_THREADS, 0, st>>>(p);
-  KQ_CHECK_LAUNCH();
-  return KRONQ_OK;
+  return launch_kernel(st, distill_kernel<T, FWD, BWD>, n, DI_THREADS, 0, 1, false, p);
 }
 
 template <class T>

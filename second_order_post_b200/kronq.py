@@ -303,24 +303,25 @@ def _view(name, t, rows, cols, dev, dtype=torch.bfloat16):
     """(pointer, row stride) of an optional matrix, checked."""
     if t is None:
         return None, cols + 7 & -8
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.shape == (rows, cols) and t.device == dev:
+        s0, s1 = t.stride()
+        if s1 == 1 or cols <= 1:
+            return t.data_ptr(), (s0 if rows > 1 else cols + 7 & -8)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {rows} x {cols}, not {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, not on {dev}")
-    s0, s1 = t.stride()
-    if cols > 1 and s1 != 1:
-        raise ValueError(f"{name} must have contiguous rows, not strides {(s0, s1)}")
-    return t.data_ptr(), (s0 if rows > 1 else cols + 7 & -8)
+    raise ValueError(f"{name} must have contiguous rows, not strides {t.stride()}")
 
 
 def _vector(name, t, n, dev, dtype=torch.float32):
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be {n} contiguous values, not {tuple(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, not on {dev}")
@@ -328,28 +329,39 @@ def _vector(name, t, n, dev, dtype=torch.float32):
 
 
 def _info(info, dev):
-    if info.dtype != torch.int32 or info.numel() < 1 or info.device != dev:
+    if info.dtype is not torch.int32 or info.device != dev or info.numel() < 1:
         raise ValueError(f"info must be an int32 word on {dev}")
     return info.data_ptr()
 
 
 def _device(t, name):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     return t.device
 
 
 def _enqueue(fn, dev, stream, *args):
     """Calls the library with `dev` current, on `stream` or dev's current one."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, not on {dev}")
-    if dev.index != torch.cuda.current_device():
+    index = dev.index
+    if index != _current_device():
         with torch.cuda.device(dev):
             return _enqueue(fn, dev, stream, *args)
-    st = torch.cuda.current_stream() if stream is None else stream
-    status = getattr(_lib, fn)(st.cuda_stream, *args)
+    if stream is None:
+        raw = _current_stream(index)
+    elif stream.device == dev:
+        raw = stream.cuda_stream
+    else:
+        raise ValueError(f"the stream is on {stream.device}, not on {dev}")
+    status = fn(raw, *args)
     if status != KRONQ_OK:
-        raise KronqError(fn, status)
+        raise KronqError(fn.__name__, status)
+
+
+# the current device and the handle of its current stream, without building a
+# Stream object per call (a token's call takes less time than that)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def kronq_linear(X, W, Y, info, bias=None, act=KRONQ_ACT_NONE, Z=None, R=None, stream=None):
@@ -363,7 +375,7 @@ def kronq_linear(X, W, Y, info, bias=None, act=KRONQ_ACT_NONE, Z=None, R=None, s
     x, w = _view("X", X, n, d_in, dev), _view("W", W, d_out, d_in, dev)
     z, r = _view("Z", Z, n, d_out, dev), _view("R", R, n, d_out, dev)
     y = _view("Y", Y, n, d_out, dev)
-    _enqueue("kronq_linear", dev, stream, x[0], n, d_in, x[1], w[0], d_out, w[1],
+    _enqueue(_lib.kronq_linear, dev, stream, x[0], n, d_in, x[1], w[0], d_out, w[1],
              _vector("bias", bias, d_out, dev), act, z[0], z[1], r[0], r[1], y[0], y[1],
              _info(info, dev))
 
@@ -383,7 +395,7 @@ def kronq_linear_bwd(dY, X, W, info, act=KRONQ_ACT_NONE, Z=None, dZ=None, db=Non
     x, w = _view("X", X, n, d_in, dev), _view("W", W, d_out, d_in, dev)
     dz, dxr = _view("dZ", dZ, n, d_out, dev), _view("dXr", dXr, n, d_in, dev)
     dx, dw = _view("dX", dX, n, d_in, dev), _view("dW", dW, d_out, d_in, dev)
-    _enqueue("kronq_linear_bwd", dev, stream, dy[0], dy[1], z[0], z[1], act, x[0], x[1], w[0],
+    _enqueue(_lib.kronq_linear_bwd, dev, stream, dy[0], dy[1], z[0], z[1], act, x[0], x[1], w[0],
              w[1], n, d_in, d_out, dz[0], dz[1], _vector("db", db, d_out, dev), dxr[0], dxr[1],
              dx[0], dx[1], dw[0], dw[1], _info(info, dev))
 
@@ -407,7 +419,7 @@ def kronq_gated(X, Wg, Wu, H, info, act=KRONQ_ACT_SILU, A=None, U=None, stream=N
     x, h = _view("X", X, n, d, dev), _view("H", H, n, f, dev)
     wg, wu = _view("Wg", Wg, f, d, dev), _view("Wu", Wu, f, d, dev)
     a, u = _view("A", A, n, f, dev), _view("U", U, n, f, dev)
-    _enqueue("kronq_gated", dev, stream, x[0], n, d, x[1], wg[0], wu[0], f,
+    _enqueue(_lib.kronq_gated, dev, stream, x[0], n, d, x[1], wg[0], wu[0], f,
              _pair("Wg and Wu", wg, wu), act, a[0], u[0], _pair("A and U", a, u), h[0], h[1],
              _info(info, dev))
 
@@ -426,7 +438,7 @@ def kronq_gated_bwd(dH, A, U, X, Wg, Wu, Gg, Gu, info, act=KRONQ_ACT_SILU, dX=No
     gg, gu = _view("Gg", Gg, n, f, dev), _view("Gu", Gu, n, f, dev)
     dx, dxr = _view("dX", dX, n, d, dev), _view("dXr", dXr, n, d, dev)
     dwg, dwu = _view("dWg", dWg, f, d, dev), _view("dWu", dWu, f, d, dev)
-    _enqueue("kronq_gated_bwd", dev, stream, dh[0], dh[1], a[0], u[0], _pair("A and U", a, u),
+    _enqueue(_lib.kronq_gated_bwd, dev, stream, dh[0], dh[1], a[0], u[0], _pair("A and U", a, u),
              act, x[0], x[1], wg[0], wu[0], _pair("Wg and Wu", wg, wu), n, d, f, gg[0], gu[0],
              _pair("Gg and Gu", gg, gu), dxr[0], dxr[1], dx[0], dx[1], dwg[0], dwu[0],
              _pair("dWg and dWu", dwg, dwu), _info(info, dev))
@@ -449,7 +461,7 @@ def kronq_distill_fwd(Z, T, idx, loss, lse, info, tau=1.0, weight=None, stream=N
     idx (n x k int32, negative: padding). Rows of weight 0 do not count."""
     dev = _device(Z, "Z")
     n = Z.shape[0]
-    _enqueue("kronq_distill_fwd", dev, stream, *_distill_args(Z, T, idx, tau, weight, dev),
+    _enqueue(_lib.kronq_distill_fwd, dev, stream, *_distill_args(Z, T, idx, tau, weight, dev),
              _vector("loss", loss, n, dev), _vector("lse", lse, n, dev), _info(info, dev))
 
 
@@ -459,7 +471,7 @@ def kronq_distill_bwd(Z, T, idx, lse, dZ, info, tau=1.0, weight=None, stream=Non
     dev = _device(Z, "Z")
     n, vocab = Z.shape
     dz = _view("dZ", dZ, n, vocab, dev, Z.dtype)
-    _enqueue("kronq_distill_bwd", dev, stream, *_distill_args(Z, T, idx, tau, weight, dev),
+    _enqueue(_lib.kronq_distill_bwd, dev, stream, *_distill_args(Z, T, idx, tau, weight, dev),
              _vector("lse", lse, n, dev), dz[0], max(dz[1], vocab), _info(info, dev))
 
 
@@ -469,7 +481,7 @@ def kronq_distill_step(Z, T, idx, loss, lse, dZ, info, tau=1.0, weight=None, str
     dev = _device(Z, "Z")
     n, vocab = Z.shape
     dz = _view("dZ", dZ, n, vocab, dev, Z.dtype)
-    _enqueue("kronq_distill_step", dev, stream, *_distill_args(Z, T, idx, tau, weight, dev),
+    _enqueue(_lib.kronq_distill_step, dev, stream, *_distill_args(Z, T, idx, tau, weight, dev),
              _vector("loss", loss, n, dev), _vector("lse", lse, n, dev), dz[0],
              max(dz[1], vocab), _info(info, dev))
 
