@@ -628,31 +628,82 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const ActBwdP p) {
   }
 }
 
-// db = column sums of dY * act'(Z): a CTA owns 32 columns and walks all rows,
-// 8 rows at a time (one warp a row); the warps meet in a fixed order.
+// The same with db = column sums of dZ before its rounding: a cluster of CTAs
+// owns 64 columns, each of its CTAs every (cluster size)-th band of 32 rows;
+// a thread sums 8 columns of its rows, and the threads and then the CTAs meet
+// in a fixed order (the first CTA reads the others' sums through distributed
+// shared memory). Bound by reading dY and Z and writing dZ once.
+constexpr int BG_MAXC = 8;
 template <int ACT>
-__global__ void __launch_bounds__(256)
-    bias_grad_kernel(const __nv_bfloat16 *dY, int64_t lddy, const __nv_bfloat16 *Z, int64_t ldz,
-                     int64_t n, int64_t w, float *db) {
-  __shared__ float part[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = blockIdx.x * int64_t(32) + lane;
-  float s = 0.f;
-  if (c < w) {
-    for (int64_t r = warp; r < n; r += 8) {
-      float h, dh = 1.f;
-      if (ACT != KRONQ_ACT_NONE) act_df<ACT>(__bfloat162float(Z[r * ldz + c]), h, dh);
-      s = fmaf(__bfloat162float(dY[r * lddy + c]), dh, s);
+__global__ void __launch_bounds__(256) bias_grad_kernel(const ActBwdP p, float *db, int parts) {
+  __shared__ __align__(16) float part[32][64];
+  const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
+  const int rank = blockIdx.x % parts;
+  const int64_t c = blockIdx.x / parts * int64_t(64) + 8 * cg;
+  const int n = static_cast<int>(kq_max<int64_t>(kq_min<int64_t>(8, p.w - c), 0));
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (n > 0) {
+    const int64_t step = 32 * parts;
+    constexpr int U = 4;   // rows in flight
+    for (int64_t r0 = rank * 32 + rl; r0 < p.n; r0 += U * step) {
+      float g[U][8], z[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t r = r0 + u * step;
+        if (r >= p.n) continue;
+        load8(p.dY + r * p.lddy + c, g[u], n);
+        if (ACT != KRONQ_ACT_NONE) load8(p.Z + r * p.ldz + c, z[u], n);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t r = r0 + u * step;
+        if (r >= p.n) continue;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          if (ACT != KRONQ_ACT_NONE) {
+            float h, dh;
+            act_df<ACT>(z[u][t], h, dh);
+            g[u][t] *= dh;
+          }
+          sum[t] += g[u][t];
+        }
+        if (p.G) store8(p.G + r * p.ldg + c, g[u], n);
+      }
     }
   }
-  part[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < w) {
-    float t = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t += part[k][lane];
-    db[c] = t;
+  for (int t = 0; t < 8; ++t) part[rl][8 * cg + t] = sum[t];
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) s += part[k][threadIdx.x];
+    part[0][threadIdx.x] = s;   // only this thread reads the column
   }
+  if (parts > 1) {
+    __syncwarp();
+    cluster_sync_all();
+  } else {
+    __syncthreads();
+  }
+  const int64_t col = blockIdx.x / parts * int64_t(64) + 4 * threadIdx.x;
+  if (rank == 0 && threadIdx.x < 16 && col < p.w) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) {
+      const uint32_t at = smem_u32(&part[0][4 * threadIdx.x]);
+      const float4 v = ld_dsmem_f4(parts > 1 ? mapa_shared(at, k) : at);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (col + t < p.w) db[col + t] = v[t];
+  }
+  __syncwarp();
+  if (parts > 1) cluster_sync_all();   // the others' sums stay until they are read
 }
 
 // Calls f with the activation as a compile-time constant.
@@ -840,17 +891,8 @@ kronq_status linear_bwd(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out,
     if (db) KQ_CUDA(cudaMemsetAsync(db, 0, d_out * 4, st));
     return dW.p ? zero_rows(st, dW, d_out, d_in) : KRONQ_OK;
   }
-  if (db) {  // before dZ is written: it may be dY or Z
-    KQ_TRY(with_act(act, [&](auto a) {
-      bias_grad_kernel<decltype(a)::value>
-          <<<static_cast<unsigned>(ceil_div(d_out, 32)), 256, 0, st>>>(bf(dY.p), dY.ld, bf(Z.p),
-                                                                       Z.ld, n, d_out, db);
-      KQ_CHECK_LAUNCH();
-      return KRONQ_OK;
-    }));
-  }
-  Mat G = dY;
-  if (act != KRONQ_ACT_NONE || (dZ.p && dZ.p != dY.p)) {
+  const bool write = act != KRONQ_ACT_NONE || (dZ.p && dZ.p != dY.p);
+  if (db || write) {
     ActBwdP p = {};
     p.n = n;
     p.w = d_out;
@@ -858,13 +900,17 @@ kronq_status linear_bwd(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out,
     p.lddy = dY.ld;
     p.Z = bf(Z.p);
     p.ldz = Z.ld;
-    p.G = bf(dZ.p);
+    p.G = write ? bf(dZ.p) : nullptr;
     p.ldg = dZ.ld;
     KQ_TRY(with_act(act, [&](auto a) {
-      return launch_act_bwd<decltype(a)::value, false>(st, p);
+      constexpr int ACT = decltype(a)::value;
+      if (!db) return launch_act_bwd<ACT, false>(st, p);
+      const int parts = static_cast<int>(kq_min<int64_t>(BG_MAXC, ceil_div(n, 128)));
+      return launch_kernel(st, bias_grad_kernel<ACT>, ceil_div(d_out, 64) * parts, 256, 0, parts,
+                           false, p, db, parts);
     }));
-    G = dZ;
   }
+  const Mat G = write ? dZ : dY;
   if (dX.p)
     KQ_TRY(input_grad(st, n, d_in, d_out, Operands{G, W, Mat{}, Mat{}}, dXr, dX, info));
   if (dW.p) KQ_TRY(weight_grad(st, n, d_in, d_out, G, X, dW, info));
