@@ -50,63 +50,6 @@ __device__ __forceinline__ void load_panel(uint8_t *dst, const CUtensorMap *map,
   }
 }
 
-// 32 consecutive outputs of a row to (or from) global memory; `n` of them
-// exist. Rows are 16-byte aligned at multiples of 8 elements.
-__device__ __forceinline__ void store32(__nv_bfloat16 *p, const float *v, int n) {
-  if (n >= 32) {
-    uint4 o[4];
-    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(o);
-#pragma unroll
-    for (int t = 0; t < 16; ++t) h[t] = __floats2bfloat162_rn(v[2 * t], v[2 * t + 1]);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) reinterpret_cast<uint4 *>(p)[t] = o[t];
-  } else {
-#pragma unroll
-    for (int t = 0; t < 32; ++t)
-      if (t < n) p[t] = __float2bfloat16_rn(v[t]);
-  }
-}
-__device__ __forceinline__ void add32(const __nv_bfloat16 *p, float *v, int n) {
-  if (n >= 32) {
-    uint4 o[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) o[t] = reinterpret_cast<const uint4 *>(p)[t];
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(o);
-#pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      const float2 f = __bfloat1622float2(h[t]);
-      v[2 * t] += f.x;
-      v[2 * t + 1] += f.y;
-    }
-  } else {
-#pragma unroll
-    for (int t = 0; t < 32; ++t)
-      if (t < n) v[t] += __bfloat162float(p[t]);
-  }
-}
-
-// The epilogue of 32 consecutive columns of a row: v the accumulator (gated: v
-// of the gate, u of the up projection), n of them in range.
-template <bool GATED, int ACT>
-__device__ __forceinline__ void finish32(const DenseP &p, int64_t row, int64_t col, int n,
-                                         float *v, float *u) {
-  if (!GATED && p.bias) {
-#pragma unroll
-    for (int t = 0; t < 32; ++t) v[t] += t < n ? __ldg(p.bias + col + t) : 0.f;
-  }
-  if (p.Z) store32(p.Z + row * p.ldz + col, v, n);
-  if constexpr (GATED) {
-    if (p.Z) store32(p.Z2 + row * p.ldz + col, u, n);
-#pragma unroll
-    for (int t = 0; t < 32; ++t) v[t] = act_f<ACT>(v[t]) * u[t];
-  } else {
-#pragma unroll
-    for (int t = 0; t < 32; ++t) v[t] = act_f<ACT>(v[t]);
-    if (p.R) add32(p.R + row * p.ldr + col, v, n);
-  }
-  store32(p.Y + row * p.ldy + col, v, n);
-}
-
 // ---------------------------------------------------------------- few tokens
 // For few tokens the sides change places: 128 weight rows are the MMA's M and
 // up to NT tokens its N, so that a tile wastes no tensor work on absent rows
@@ -351,12 +294,17 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
 // shared-memory traffic for 128 x 256 x 64 products: half of what one CTA
 // alone would load. The kernel is persistent: TMEM holds two accumulators,
 // and the epilogue of one tile runs while the next one accumulates.
-//   warps 0..7  epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and half
-//               w / 4 of the tile's columns
+//   warps 0..7  epilogue: warp w takes TMEM lanes 32 (w % 4) .. + 31 (rows) and
+//               half w / 4 of the tile's columns, 64 at a time: two slots of 4 KB
+//               collect 32 rows x 64 columns of an output, which one TMA store
+//               takes out (stores straight from the row-per-lane registers
+//               touch 32 rows an instruction and took 5000 cycles a tile).
+//               Residual values come into the same slot by asynchronous
+//               copies, the first before the accumulator is ready.
 //   warp 8      TMA producer (each CTA loads its own panels; the bytes of both
 //               are counted on the even CTA's barrier)
 //   warp 9      TMEM owner; in the even CTA the MMA issuer
-constexpr int PSTAGES = 6;
+constexpr int PSTAGES = 5;
 constexpr int PSTAGE = 2 * DPANEL;
 constexpr int PTHREADS = 320;
 constexpr int PGROUP = 8;                // tile raster: row tiles per band
@@ -370,7 +318,71 @@ struct PairCtl {
   uint32_t tmem_base;
   int abort;
 };
-constexpr int PSMEM = PSTAGES * PSTAGE + 1024 + int(sizeof(PairCtl)) + 64;
+constexpr int PSLOT = 32 * 128;            // staging slot: 32 rows of 64 bf16
+constexpr int PSMEM = PSTAGES * PSTAGE + 16 * PSLOT + 1024 + int(sizeof(PairCtl)) + 64;
+
+// Output maps of the pair kernel: Y, and the kept pre-activations.
+struct OutMaps {
+  CUtensorMap y, z, z2;
+};
+
+// Columns [32 h, 32 h + 32) of lane's row in a staging slot (128-byte rows,
+// 16-byte granules swizzled by the row's low bits, as the TMA maps have it).
+__device__ __forceinline__ void stage32(uint8_t *slot, int lane, int h, const float *v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint4 o;
+    __nv_bfloat162 *b = reinterpret_cast<__nv_bfloat162 *>(&o);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) b[t] = __floats2bfloat162_rn(v[8 * j + 2 * t], v[8 * j + 2 * t + 1]);
+    *reinterpret_cast<uint4 *>(slot + lane * 128 + ((4 * h + j) ^ (lane & 7)) * 16) = o;
+  }
+}
+__device__ __forceinline__ void add_staged32(const uint8_t *slot, int lane, int h, float *v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 o =
+        *reinterpret_cast<const uint4 *>(slot + lane * 128 + ((4 * h + j) ^ (lane & 7)) * 16);
+    const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&o);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float2 f = __bfloat1622float2(b[t]);
+      v[8 * j + 2 * t] += f.x;
+      v[8 * j + 2 * t + 1] += f.y;
+    }
+  }
+}
+// Takes a staged slot out to (col, row) of an M x N matrix; the slot is free
+// again after slot_free. A TMA store leaves out what lies outside its map in
+// whole 16-byte granules only, so the maps end at the last multiple of 8
+// columns, and the lanes write their rows' last N % 8 columns themselves.
+__device__ __forceinline__ void slot_out(const CUtensorMap *map, __nv_bfloat16 *y, int64_t ld,
+                                         int64_t M, int64_t N, const uint8_t *slot, int lane,
+                                         int64_t col, int64_t row) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  const int64_t n8 = N & ~int64_t(7);
+  if (lane == 0 && col < n8) {
+    tma_store_2d(map, slot, static_cast<int32_t>(col), static_cast<int32_t>(row));
+    bulk_commit();
+  }
+  if (n8 < N && n8 - col < 64 && n8 >= col && row + lane < M) {
+    const int j = static_cast<int>(n8 - col) / 8;
+    const __nv_bfloat16 *v =
+        reinterpret_cast<const __nv_bfloat16 *>(slot + lane * 128 + (j ^ (lane & 7)) * 16);
+    for (int t = 0; t < N - n8; ++t) y[(row + lane) * ld + n8 + t] = v[t];
+  }
+}
+// Waits until all but the warp's last store (ALL: every store) have read their
+// slots.
+template <bool ALL>
+__device__ __forceinline__ void slot_free(int lane) {
+  if (lane == 0) {
+    if constexpr (ALL) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+  }
+  __syncwarp();
+}
 
 __device__ __forceinline__ void load_panel_pair(uint8_t *dst, const CUtensorMap *map,
                                                 uint32_t bar, bool mn, int32_t r0, int32_t k0) {
@@ -398,12 +410,13 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmA2,
-                      const __grid_constant__ CUtensorMap tmB2, const DenseP p) {
+                      const __grid_constant__ CUtensorMap tmB2,
+                      const __grid_constant__ OutMaps out, const DenseP p) {
   constexpr int NT = GATED ? 128 : 256;   // columns of the output per tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  PairCtl *ctl = reinterpret_cast<PairCtl *>(smem + PSTAGES * PSTAGE);
+  PairCtl *ctl = reinterpret_cast<PairCtl *>(smem + PSTAGES * PSTAGE + 16 * PSLOT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int64_t cluster = cluster_id_x(), clusters = gridDim.x / 2;
@@ -500,31 +513,96 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     }
   } else {
     const int q = warp & 3, half = warp >> 2;
+    uint8_t *slots = smem + PSTAGES * PSTAGE + 2 * warp * PSLOT;
+    uint32_t used = 0;   // outputs taken out so far: they use the two slots in turn
     int i = 0;
     for (int64_t t = cluster; t < tiles; t += clusters, ++i) {
       const int a = i & 1;
+      int64_t bi, bj;
+      pair_tile(t, p.tiles_m, tiles_n, bi, bj);
+      const int64_t row0 = bi * 256 + 128 * rank + 32 * q;   // this warp's rows
+      // residual values of columns [col, col + 64) into a slot
+      auto residual = [&](uint8_t *slot, int64_t col) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + (lane >> 3), j = lane & 7;
+          const int64_t row = row0 + r, c = col + 8 * j;
+          const int bytes =
+              row < p.M ? static_cast<int>(kq_max<int64_t>(kq_min<int64_t>(p.N - c, 8), 0)) * 2 : 0;
+          cp_async16(smem_u32(slot + r * 128 + (j ^ (r & 7)) * 16),
+                     bytes > 0 ? p.R + row * p.ldr + c : p.R, bytes);
+        }
+      };
+      const bool early = !GATED && p.R && !p.Z;   // the first output takes R
+      if (early) {
+        slot_free<false>(lane);
+        residual(slots + (used & 1) * PSLOT, bj * NT + half * (NT / 2));
+      }
       const bool ok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      int64_t bi, bj;
-      pair_tile(t, p.tiles_m, tiles_n, bi, bj);
-      const int64_t row = bi * 256 + 128 * rank + 32 * q + lane;
-      for (int c = 0; c < NT / 64; ++c) {
-        const int cc = half * (NT / 2) + 32 * c;
+      for (int c = 0; c < NT / 128; ++c) {
+        const int cc = half * (NT / 2) + 64 * c;
         const int64_t col = bj * NT + cc;
-        if (col >= p.N) break;
-        const int n = static_cast<int>(kq_min<int64_t>(32, p.N - col));
+        if (col >= p.N || row0 >= p.M) break;
         const uint32_t ta = tbase + (static_cast<uint32_t>(32 * q) << 16) + 256 * a + cc;
-        float v[32], u[GATED ? 32 : 1];
-        tmem_ld32(ta, v);
-        if constexpr (GATED) tmem_ld32(ta + 128, u);
-        if (row < p.M) finish32<GATED, ACT>(p, row, col, n, v, u);
-        __syncwarp();
+        if (p.Z) {
+#pragma unroll
+          for (int o = 0; o < (GATED ? 2 : 1); ++o) {
+            uint8_t *slot = slots + (used++ & 1) * PSLOT;
+            slot_free<false>(lane);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float v[32];
+              tmem_ld32(ta + 128 * o + 32 * h, v);
+              if (!GATED && p.bias) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  v[k] += col + 32 * h + k < p.N ? __ldg(p.bias + col + 32 * h + k) : 0.f;
+              }
+              stage32(slot, lane, h, v);
+            }
+            slot_out(o ? &out.z2 : &out.z, o ? p.Z2 : p.Z, p.ldz, p.M, p.N, slot, lane, col, row0);
+          }
+        }
+        uint8_t *slot = slots + (used++ & 1) * PSLOT;
+        if (!early || c > 0) {
+          slot_free<false>(lane);
+          if (!GATED && p.R) residual(slot, col);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[32], u[GATED ? 32 : 1];
+          tmem_ld32(ta + 32 * h, v);
+          if constexpr (GATED) tmem_ld32(ta + 128 + 32 * h, u);
+          if (!GATED && p.bias) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              v[k] += col + 32 * h + k < p.N ? __ldg(p.bias + col + 32 * h + k) : 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            v[k] = act_f<ACT>(v[k]);
+            if constexpr (GATED) v[k] *= u[k];
+          }
+          if (!GATED && p.R) {
+            if (h == 0) {
+              cp_async_wait();
+              __syncwarp();
+            }
+            add_staged32(slot, lane, h, v);
+          }
+          stage32(slot, lane, h, v);
+        }
+        slot_out(&out.y, p.Y, p.ldy, p.M, p.N, slot, lane, col, row0);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tempty[a]), 0));
     }
+    // the slots are read before the CTA ends (the stores complete with the grid)
+    cp_async_wait();
+    slot_free<true>(lane);
   }
 
   // ---- teardown: after an abort make sure no copy or MMA is still in flight
@@ -752,8 +830,14 @@ kronq_status launch_pair(cudaStream_t st, const CUtensorMap *tm, DenseP p) {
   p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
   const int64_t tiles = p.tiles_m * ceil_div(p.N, GATED ? 128 : 256);
   const int64_t clusters = kq_min<int64_t>(tiles, 74);
+  OutMaps out;
+  memset(&out, 0, sizeof(out));
+  const int64_t n8 = p.N & ~int64_t(7);
+  if (n8) KQ_TRY(make_tmap_2d(&out.y, p.Y, true, n8, p.M, p.ldy, 64, 32));
+  if (n8 && p.Z) KQ_TRY(make_tmap_2d(&out.z, p.Z, true, n8, p.M, p.ldz, 64, 32));
+  if (n8 && p.Z2) KQ_TRY(make_tmap_2d(&out.z2, p.Z2, true, n8, p.M, p.ldz, 64, 32));
   return launch_kernel(st, kern, 2 * clusters, PTHREADS, PSMEM, 2, true, tm[0], tm[1], tm[2],
-                       tm[3], p);
+                       tm[3], out, p);
 }
 
 // Tokens per tile of the few-token kernel, 0 for the pair kernel.
