@@ -178,6 +178,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same without ever waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Same test, but the thread may sleep in hardware until the phase completes
 // or about `ns` nanoseconds pass (no polling traffic on shared memory).
 __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t *bar, uint32_t parity,
@@ -356,13 +369,14 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc,
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrive on the barrier at this offset in both CTAs of the pair once all
-// previously issued pair MMAs of this thread finish.
-__device__ __forceinline__ void umma_commit_pair(uint64_t *bar) {
+// Arrive on the barrier at this offset in both CTAs of the pair (cluster ranks
+// leader and leader + 1) once all previously issued pair MMAs of this thread
+// finish.
+__device__ __forceinline__ void umma_commit_pair(uint64_t *bar, int leader) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3 << leader))
       : "memory");
 }
 // Arrive on a barrier of another CTA of the cluster.

@@ -161,28 +161,31 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
     }
   } else if (warp == 1 && lane == 0) {
     const uint32_t idesc = idesc_make(1, W_MN, 0, DT, NT);
-    bool ok = true;
+    const uint32_t w0 = smem_u32(smem), x0 = w0 + DPANEL * (GATED ? 2 : 1);
+    const uint64_t dw0 = W_MN ? sdesc_sw128(w0, DBOX, 1024) : sdesc_sw128(w0, 16, 1024);
+    const uint64_t dx0 = sdesc_sw128(x0, 16, 1024);
+    // (the next slab is looked for before this one's commit: see the pair kernel)
+    bool ok = true, landed = false;
+    int s = 0;
+    uint32_t parity = 0;
     for (int it = 0; it < cnt; ++it) {
-      const int s = it % C::STAGES;
-      if (!mbar_wait(&ctl->full[s], (it / C::STAGES) & 1, abort)) {
+      if (!landed && !mbar_wait(&ctl->full[s], parity, abort)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t w0 = smem_u32(smem + s * C::STAGE);
-      const uint32_t x0 = w0 + DPANEL * (GATED ? 2 : 1);
+      const uint32_t at = s * (C::STAGE >> 4);
 #pragma unroll
       for (int kk = 0; kk < DBK / 16; ++kk) {
-        const uint64_t dx = sdesc_sw128(x0 + kk * 32, 16, 1024);
 #pragma unroll
-        for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-          const uint32_t w = w0 + h * DPANEL;
-          const uint64_t dw = W_MN ? sdesc_sw128(w + kk * 2048, DBOX, 1024)
-                                   : sdesc_sw128(w + kk * 32, 16, 1024);
-          umma_bf16(tbase + NT * h, dw, dx, idesc, (it | kk) != 0);
-        }
+        for (int h = 0; h < (GATED ? 2 : 1); ++h)
+          umma_bf16(tbase + NT * h, dw0 + at + h * (DPANEL >> 4) + kk * (W_MN ? 128 : 2),
+                    dx0 + at + kk * 2, idesc, (it | kk) != 0);
       }
-      umma_commit(&ctl->empty[s]);
+      uint64_t *used = &ctl->empty[s];
+      if (++s == C::STAGES) s = 0, parity ^= 1;
+      landed = mbar_test(&ctl->full[s], parity);
+      umma_commit(used);
     }
     if (ok) umma_commit(&ctl->done);
   }
@@ -394,6 +397,12 @@ __device__ __forceinline__ void load_panel_pair(uint8_t *dst, const CUtensorMap 
   }
 }
 
+// With few tiles (SPLIT) the k range of a tile is divided over the pairs of a
+// larger cluster: every CTA writes its 128 x 256 partial sums to the ring's
+// shared memory (128 KB of fp32, 16-byte granules swizzled by the row), and
+// after a cluster barrier each pair sums and finishes its share of the columns
+// over all parts, in the order of their ranks, through distributed shared
+// memory. One tile a cluster.
 // Row and column tile of tile t: bands of PGROUP row tiles, column by column,
 // so that the tiles in flight share their panels through L2.
 __device__ __forceinline__ void pair_tile(int64_t t, int tiles_m, int tiles_n, int64_t &bi,
@@ -405,7 +414,7 @@ __device__ __forceinline__ void pair_tile(int64_t t, int tiles_m, int tiles_n, i
   bj = r / rows;
 }
 
-template <bool GATED, int ACT, bool A_MN, bool B_MN>
+template <bool GATED, int ACT, bool A_MN, bool B_MN, int S>
 __global__ void __launch_bounds__(PTHREADS, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
@@ -418,11 +427,14 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   PairCtl *ctl = reinterpret_cast<PairCtl *>(smem + PSTAGES * PSTAGE + 16 * PSLOT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int64_t cluster = cluster_id_x(), clusters = gridDim.x / 2;
+  constexpr bool SPLIT = S > 1;           // S pairs in the cluster
+  const int crank = static_cast<int>(cluster_ctarank());
+  const int rank = crank & 1, part = SPLIT ? crank >> 1 : 0, leader = crank & ~1;
+  const int64_t cluster = cluster_id_x(), clusters = gridDim.x / (2 * S);
   const int tiles_n = static_cast<int>((p.N + NT - 1) / NT);
   const int64_t tiles = int64_t(p.tiles_m) * tiles_n;
-  const int nk = p.nk1 * p.nseg;
+  const int nk_all = p.nk1 * p.nseg, kb = SPLIT ? nk_all * part / S : 0;
+  const int nk = SPLIT ? nk_all * (part + 1) / S - kb : nk_all;   // this pair's k-slabs
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < PSTAGES; ++s) {
@@ -449,78 +461,163 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   pdl_launch();
   pdl_wait();
 
-  int64_t issued = 0;
+  // ring position: slot s, and the parity of its current round
+  uint32_t issued = 0;
   if (warp == 8) {
     if (lane == 0) {
-      int64_t g = 0;
+      int s = 0;
+      uint32_t round = 0;
       bool ok = true;
+      const uint32_t full0 = mapa_shared(smem_u32(&ctl->full[0]), leader);
       for (int64_t t = cluster; t < tiles && ok; t += clusters) {
         int64_t bi, bj;
         pair_tile(t, p.tiles_m, tiles_n, bi, bj);
         const int32_t m0 = static_cast<int32_t>(bi * 256 + 128 * rank);
         const int32_t n0 = static_cast<int32_t>(bj * NT + (GATED ? 0 : 128 * rank));
-        for (int it = 0; it < nk; ++it, ++g) {
-          const int s = static_cast<int>(g % PSTAGES);
-          if (g >= PSTAGES && !mbar_wait(&ctl->empty[s], ((g / PSTAGES) - 1) & 1, abort)) {
+        for (int it = 0; it < nk; ++it) {
+          if (round > 0 && !mbar_wait(&ctl->empty[s], (round - 1) & 1, abort)) {
             ok = false;
             break;
           }
           uint8_t *st = smem + s * PSTAGE;
-          const bool second = it >= p.nk1;
-          const int32_t k0 = (second ? it - p.nk1 : it) * DBK;
-          const uint32_t bar = mapa_shared(smem_u32(&ctl->full[s]), 0);
+          const bool second = kb + it >= p.nk1;
+          const int32_t k0 = (second ? kb + it - p.nk1 : kb + it) * DBK;
+          const uint32_t bar = full0 + s * 8;
           if (rank == 0) mbar_expect_tx(&ctl->full[s], 2 * PSTAGE);
           load_panel_pair(st, second ? &tmA2 : &tmA, bar, A_MN, m0, k0);
           load_panel_pair(st + DPANEL, (GATED ? rank != 0 : second) ? &tmB2 : &tmB, bar, B_MN, n0,
                           k0);
-          issued = g + 1;
+          ++issued;
+          if (++s == PSTAGES) s = 0, ++round;
         }
       }
       // every arrival on this CTA's barriers has landed before the CTA ends
-      for (int64_t e = kq_max<int64_t>(g - PSTAGES, 0); e < g && ok; ++e)
+      for (uint32_t e = issued > PSTAGES ? issued - PSTAGES : 0; e < issued && ok; ++e)
         ok = mbar_wait(&ctl->empty[e % PSTAGES], (e / PSTAGES) & 1, abort);
     }
   } else if (warp == 9) {
     if (rank == 0 && lane == 0) {
       const uint32_t idesc = idesc_make(1, A_MN, B_MN, 256, 256);
-      int64_t g = 0;
-      int i = 0;
-      bool ok = true;
+      // descriptors of slot 0's first step; others differ in the address field
+      const uint32_t a0 = smem_u32(smem), b0 = a0 + DPANEL;
+      const uint64_t da0 = A_MN ? sdesc_sw128(a0, DBOX, 1024) : sdesc_sw128(a0, 16, 1024);
+      const uint64_t db0 = B_MN ? sdesc_sw128(b0, DBOX, 1024) : sdesc_sw128(b0, 16, 1024);
+      // A barrier wait behind a commit holds the thread until the MMAs before
+      // the commit are done (measured: 560 cycles a slab of 4 MMAs whatever
+      // their width, 512 without waits at 256 columns). So the next slab is
+      // looked for before this one's commit; only a slab that is late is
+      // waited for behind it.
+      int s = 0, i = 0;
+      uint32_t parity = 0;
+      bool ok = true, landed = false;
       for (int64_t t = cluster; t < tiles && ok; t += clusters, ++i) {
         const int a = i & 1;
         if (i >= 2 && !mbar_wait(&ctl->tempty[a], ((i >> 1) - 1) & 1, abort)) break;
-        tc_fence_after();
-        for (int it = 0; it < nk; ++it, ++g) {
-          const int s = static_cast<int>(g % PSTAGES);
-          if (!mbar_wait(&ctl->full[s], (g / PSTAGES) & 1, abort)) {
+        for (int it = 0; it < nk; ++it) {
+          if (!landed && !mbar_wait(&ctl->full[s], parity, abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + s * PSTAGE), b0 = a0 + DPANEL;
+          const uint32_t at = s * (PSTAGE >> 4);
 #pragma unroll
-          for (int kk = 0; kk < DBK / 16; ++kk) {
-            const uint64_t da = A_MN ? sdesc_sw128(a0 + kk * 2048, DBOX, 1024)
-                                     : sdesc_sw128(a0 + kk * 32, 16, 1024);
-            const uint64_t db = B_MN ? sdesc_sw128(b0 + kk * 2048, DBOX, 1024)
-                                     : sdesc_sw128(b0 + kk * 32, 16, 1024);
-            umma_bf16_pair(tbase + 256 * a, da, db, idesc, (it | kk) != 0);
-          }
-          umma_commit_pair(&ctl->empty[s]);
+          for (int kk = 0; kk < DBK / 16; ++kk)
+            umma_bf16_pair(tbase + 256 * a, da0 + at + kk * (A_MN ? 128 : 2),
+                           db0 + at + kk * (B_MN ? 128 : 2), idesc, (it | kk) != 0);
+          uint64_t *used = &ctl->empty[s];
+          if (++s == PSTAGES) s = 0, parity ^= 1;
+          landed = mbar_test(&ctl->full[s], parity);
+          umma_commit_pair(used, leader);
         }
-        if (ok) umma_commit_pair(&ctl->tfull[a]);
+        if (ok) umma_commit_pair(&ctl->tfull[a], leader);
       }
     }
   } else {
     const int q = warp & 3, half = warp >> 2;
     uint8_t *slots = smem + PSTAGES * PSTAGE + 2 * warp * PSLOT;
+    if constexpr (SPLIT) {
+      const bool ok = mbar_wait(&ctl->tfull[0], 0, abort);
+      const bool alive = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q) << 16);
+      if (alive) {   // this CTA's part -> shared memory
+        const int r = 32 * q + lane;
+        for (int c = 128 * half; c < 128 * half + 128; c += 32) {
+          float v[32];
+          tmem_ld32(tq + c, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4 *>(smem + r * 1024 + ((c / 4 + j) ^ (r & 7)) * 16) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      cluster_sync_all();
+      // four columns a lane, whole row segments a warp (remote reads and
+      // global stores of 256 bytes and more), 16 rows a warp in two batches
+      int64_t bi, bj;
+      pair_tile(cluster, p.tiles_m, tiles_n, bi, bj);
+      constexpr int WIDTH = NT / S, PER_ROW = WIDTH / 4, STEP = 32 / PER_ROW;
+      constexpr int U = GATED ? 8 / S : 16 / S;   // 16 remote loads in flight a lane
+      const int cc = WIDTH * part + lane % PER_ROW * 4;
+      const int64_t col = bj * NT + cc, row0 = bi * 256 + 128 * rank;
+      const int n = static_cast<int>(kq_max<int64_t>(kq_min<int64_t>(4, p.N - col), 0));
+      float bias[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) bias[k] = !GATED && p.bias && k < n ? p.bias[col + k] : 0.f;
+      uint32_t base[S];
+#pragma unroll
+      for (int o = 0; o < S; ++o) base[o] = mapa_shared(smem_u32(smem), 2 * o + rank);
+#pragma unroll 1
+      for (int r0 = warp * 16 + lane / PER_ROW; r0 < warp * 16 + 16 && alive && n > 0;
+           r0 += U * STEP) {
+        float4 x[S][U], y[S][GATED ? U : 1];
+#pragma unroll
+        for (int o = 0; o < S; ++o) {
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int r = kq_min(r0 + k * STEP, 127);
+            x[o][k] = ld_dsmem_f4(base[o] + r * 1024 + ((cc / 4) ^ (r & 7)) * 16);
+            if constexpr (GATED)
+              y[o][k] = ld_dsmem_f4(base[o] + r * 1024 + ((cc / 4 + 32) ^ (r & 7)) * 16);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int r = r0 + k * STEP;
+          const int64_t row = row0 + r;
+          if (r >= warp * 16 + 16 || row >= p.M) continue;
+          float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int o = 0; o < S; ++o) {
+            v[0] += x[o][k].x; v[1] += x[o][k].y; v[2] += x[o][k].z; v[3] += x[o][k].w;
+            if constexpr (GATED) {
+              u[0] += y[o][k].x; u[1] += y[o][k].y; u[2] += y[o][k].z; u[3] += y[o][k].w;
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) v[t] += bias[t];
+          if (p.Z) store4(p.Z + row * p.ldz + col, v, n);
+          if (GATED && p.Z) store4(p.Z2 + row * p.ldz + col, u, n);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            v[t] = act_f<ACT>(v[t]);
+            if (GATED) v[t] *= u[t];
+            else if (p.R) v[t] += t < n ? __bfloat162float(p.R[row * p.ldr + col + t]) : 0.f;
+          }
+          store4(p.Y + row * p.ldy + col, v, n);
+        }
+      }
+    }
     uint32_t used = 0;   // outputs taken out so far: they use the two slots in turn
     int i = 0;
-    for (int64_t t = cluster; t < tiles; t += clusters, ++i) {
+    for (int64_t t = cluster; t < tiles && !SPLIT; t += clusters, ++i) {
       const int a = i & 1;
       int64_t bi, bj;
       pair_tile(t, p.tiles_m, tiles_n, bi, bj);
       const int64_t row0 = bi * 256 + 128 * rank + 32 * q;   // this warp's rows
+      const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q) << 16) + 256 * a;
       // residual values of columns [col, col + 64) into a slot
       auto residual = [&](uint8_t *slot, int64_t col) {
 #pragma unroll
@@ -533,19 +630,19 @@ __global__ void __launch_bounds__(PTHREADS, 1)
                      bytes > 0 ? p.R + row * p.ldr + c : p.R, bytes);
         }
       };
+      const int first = half * (NT / 2);
       const bool early = !GATED && p.R && !p.Z;   // the first output takes R
       if (early) {
         slot_free<false>(lane);
-        residual(slots + (used & 1) * PSLOT, bj * NT + half * (NT / 2));
+        residual(slots + (used & 1) * PSLOT, bj * NT + first);
       }
       const bool ok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       for (int c = 0; c < NT / 128; ++c) {
-        const int cc = half * (NT / 2) + 64 * c;
+        const int cc = first + 64 * c;
         const int64_t col = bj * NT + cc;
         if (col >= p.N || row0 >= p.M) break;
-        const uint32_t ta = tbase + (static_cast<uint32_t>(32 * q) << 16) + 256 * a + cc;
         if (p.Z) {
 #pragma unroll
           for (int o = 0; o < (GATED ? 2 : 1); ++o) {
@@ -554,7 +651,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float v[32];
-              tmem_ld32(ta + 128 * o + 32 * h, v);
+              tmem_ld32(tq + cc + 128 * o + 32 * h, v);
               if (!GATED && p.bias) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
@@ -573,8 +670,8 @@ __global__ void __launch_bounds__(PTHREADS, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float v[32], u[GATED ? 32 : 1];
-          tmem_ld32(ta + 32 * h, v);
-          if constexpr (GATED) tmem_ld32(ta + 128 + 32 * h, u);
+          tmem_ld32(tq + cc + 32 * h, v);
+          if constexpr (GATED) tmem_ld32(tq + cc + 128 + 32 * h, u);
           if (!GATED && p.bias) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
@@ -598,12 +695,15 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tempty[a]), 0));
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tempty[a]), leader));
     }
     // the slots are read before the CTA ends (the stores complete with the grid)
     cp_async_wait();
     slot_free<true>(lane);
   }
+
+  __syncwarp();
+  if (SPLIT && warp >= 8) cluster_sync_all();   // the parts are written
 
   // ---- teardown: after an abort make sure no copy or MMA is still in flight
   __syncwarp();
@@ -613,15 +713,15 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     if (threadIdx.x == 0) report(p.info, KRONQ_ERR_TIMEOUT);
     if (rank == 0 && warp == 8 && lane == 0) {
       const uint64_t t0 = globaltimer();
-      for (int s = 0; s < PSTAGES && s < issued; ++s) {
-        const int64_t last = ((issued - 1 - s) / PSTAGES) * PSTAGES + s;
+      for (uint32_t s = 0; s < PSTAGES && s < issued; ++s) {
+        const uint32_t last = ((issued - 1 - s) / PSTAGES) * PSTAGES + s;
         while (!mbar_try_wait(&ctl->full[s], (last / PSTAGES) & 1) &&
                globaltimer() - t0 < kWaitLimitNs) {
         }
       }
     }
     if (rank == 0 && warp == 9 && lane == 0) {
-      umma_commit_pair(&ctl->drain);
+      umma_commit_pair(&ctl->drain, leader);
       const uint64_t t0 = globaltimer();
       while (!mbar_try_wait(&ctl->drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
       }
@@ -825,19 +925,29 @@ kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d,
 
 template <bool GATED, int ACT, bool A_MN, bool B_MN>
 kronq_status launch_pair(cudaStream_t st, const CUtensorMap *tm, DenseP p) {
-  auto *kern = dense_pair_kernel<GATED, ACT, A_MN, B_MN>;
-  KQ_TRY(smem_attr(kern, PSMEM));
   p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
   const int64_t tiles = p.tiles_m * ceil_div(p.N, GATED ? 128 : 256);
-  const int64_t clusters = kq_min<int64_t>(tiles, 74);
+  const int nk = p.nk1 * p.nseg;
   OutMaps out;
   memset(&out, 0, sizeof(out));
   const int64_t n8 = p.N & ~int64_t(7);
   if (n8) KQ_TRY(make_tmap_2d(&out.y, p.Y, true, n8, p.M, p.ldy, 64, 32));
   if (n8 && p.Z) KQ_TRY(make_tmap_2d(&out.z, p.Z, true, n8, p.M, p.ldz, 64, 32));
   if (n8 && p.Z2) KQ_TRY(make_tmap_2d(&out.z2, p.Z2, true, n8, p.M, p.ldz, 64, 32));
-  return launch_kernel(st, kern, 2 * clusters, PTHREADS, PSMEM, 2, true, tm[0], tm[1], tm[2],
-                       tm[3], out, p);
+  auto split = [&](auto s) {
+    constexpr int S = decltype(s)::value;
+    auto *kern = dense_pair_kernel<GATED, ACT, A_MN, B_MN, S>;
+    KQ_TRY(smem_attr(kern, PSMEM));
+    return launch_kernel(st, kern, tiles * 2 * S, PTHREADS, PSMEM, 2 * S, true, tm[0], tm[1],
+                         tm[2], tm[3], out, p);
+  };
+  // clusters of 8 CTAs of this size: 15 fit on the chip at once, of 4: 33
+  if (!GATED && tiles <= 15 && nk >= 16) return split(std::integral_constant<int, GATED ? 2 : 4>());
+  if (tiles <= 33 && nk >= 8) return split(std::integral_constant<int, 2>());
+  auto *kern = dense_pair_kernel<GATED, ACT, A_MN, B_MN, 1>;
+  KQ_TRY(smem_attr(kern, PSMEM));
+  return launch_kernel(st, kern, 2 * kq_min<int64_t>(tiles, 74), PTHREADS, PSMEM, 2, true, tm[0],
+                       tm[1], tm[2], tm[3], out, p);
 }
 
 // Tokens per tile of the few-token kernel, 0 for the pair kernel.
