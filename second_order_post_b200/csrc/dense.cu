@@ -29,7 +29,7 @@ constexpr int DBOX = 64 * DBK * 2;       // one MN-major box: 64 x 64
 struct DenseP {
   int64_t M, N, K;
   int nk1, nseg;               // k-stages per segment, segments
-  int tiles_m;
+  int tiles_m, act;
   const float *bias;           // linear
   __nv_bfloat16 *Z, *Z2;       // kept pre-activations (gated: A and U)
   int64_t ldz;
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   auto *ctl = reinterpret_cast<FewCtl<C::STAGES> *>(smem + C::STAGES * C::STAGE);
   static_assert(sizeof(*ctl) <= 256, "control block");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = fp.split, rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t tile = blockIdx.x / split;
   const int64_t t0 = tile % fp.tiles_t * NT, f0 = tile / fp.tiles_t * DT;
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
   pdl_wait();
 
   int issued = 0;
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && elect_one()) {
     for (int it = 0; it < cnt; ++it) {
       const int s = it % C::STAGES;
       if (it >= C::STAGES && !mbar_wait(&ctl->empty[s], ((it / C::STAGES) - 1) & 1, abort)) break;
@@ -159,12 +159,13 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
                   static_cast<int32_t>(t0));
       issued = it + 1;
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && elect_one()) {
     const uint32_t idesc = idesc_make(1, W_MN, 0, DT, NT);
     const uint32_t w0 = smem_u32(smem), x0 = w0 + DPANEL * (GATED ? 2 : 1);
     const uint64_t dw0 = W_MN ? sdesc_sw128(w0, DBOX, 1024) : sdesc_sw128(w0, 16, 1024);
     const uint64_t dx0 = sdesc_sw128(x0, 16, 1024);
-    // (the next slab is looked for before this one's commit: see the pair kernel)
+    // (the next slab's barrier is tested before this one's MMAs: see the pair
+    // kernel)
     bool ok = true, landed = false;
     int s = 0;
     uint32_t parity = 0;
@@ -175,6 +176,9 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
       }
       tc_fence_after();
       const uint32_t at = s * (C::STAGE >> 4);
+      uint64_t *used = &ctl->empty[s];
+      if (++s == C::STAGES) s = 0, parity ^= 1;
+      landed = mbar_try_wait(&ctl->full[s], parity);
 #pragma unroll
       for (int kk = 0; kk < DBK / 16; ++kk) {
 #pragma unroll
@@ -182,9 +186,6 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
           umma_bf16(tbase + NT * h, dw0 + at + h * (DPANEL >> 4) + kk * (W_MN ? 128 : 2),
                     dx0 + at + kk * 2, idesc, (it | kk) != 0);
       }
-      uint64_t *used = &ctl->empty[s];
-      if (++s == C::STAGES) s = 0, parity ^= 1;
-      landed = mbar_test(&ctl->full[s], parity);
       umma_commit(used);
     }
     if (ok) umma_commit(&ctl->done);
@@ -266,7 +267,8 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
   // ---- teardown: after an abort make sure no copy or MMA is still in flight
   if (ctl->abort) {
     if (threadIdx.x == 0) report(p.info, KRONQ_ERR_TIMEOUT);
-    if (warp == 0 && lane == 0) {
+    // (the same lanes are elected again)
+    if (warp == 0 && elect_one()) {
       const uint64_t c0 = globaltimer();
       for (int s = 0; s < C::STAGES && s < issued; ++s) {
         const int last = ((issued - 1 - s) / C::STAGES) * C::STAGES + s;
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
         }
       }
     }
-    if (warp == 1 && lane == 0) {
+    if (warp == 1 && elect_one()) {
       umma_commit(&ctl->drain);
       const uint64_t c0 = globaltimer();
       while (!mbar_try_wait(&ctl->drain, 0) && globaltimer() - c0 < kWaitLimitNs) {
@@ -307,22 +309,30 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
 //   warp 8      TMA producer (each CTA loads its own panels; the bytes of both
 //               are counted on the even CTA's barrier)
 //   warp 9      TMEM owner; in the even CTA the MMA issuer
-constexpr int PSTAGES = 5;
-constexpr int PSTAGE = 2 * DPANEL;
 constexpr int PTHREADS = 320;
 constexpr int PGROUP = 8;                // tile raster: row tiles per band
+constexpr int PSLOT = 32 * 128;          // staging slot: 32 rows of 64 bf16
 
+template <int STAGES>
 struct PairCtl {
-  uint64_t full[PSTAGES];    // both CTAs' panels landed (even CTA's is used)
-  uint64_t empty[PSTAGES];   // MMAs that read the stage finished (both CTAs)
+  uint64_t full[STAGES];     // both CTAs' panels landed (even CTA's is used)
+  uint64_t empty[STAGES];    // MMAs that read the stage finished (both CTAs)
   uint64_t tfull[2];         // accumulator complete (both CTAs)
   uint64_t tempty[2];        // read out by both CTAs' epilogues (even CTA's)
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
-constexpr int PSLOT = 32 * 128;            // staging slot: 32 rows of 64 bf16
-constexpr int PSMEM = PSTAGES * PSTAGE + 16 * PSLOT + 1024 + int(sizeof(PairCtl)) + 64;
+
+// NB: columns of the accumulator. A CTA's stage: 128 rows of A, NB / 2 of B.
+template <int NB>
+struct Pair {
+  static constexpr int STAGE = DPANEL + NB / 2 * DBK * 2;
+  static constexpr int STAGES = NB == 256 ? 5 : 6;
+  static constexpr int SMEM = STAGES * STAGE + 16 * PSLOT + 1024 + int(sizeof(PairCtl<STAGES>)) + 64;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(STAGES * STAGE >= 128 * NB * 4, "the partial sums fit in the ring");
+};
 
 // Output maps of the pair kernel: Y, and the kept pre-activations.
 struct OutMaps {
@@ -387,13 +397,15 @@ __device__ __forceinline__ void slot_free(int lane) {
   __syncwarp();
 }
 
+template <int ROWS>
 __device__ __forceinline__ void load_panel_pair(uint8_t *dst, const CUtensorMap *map,
                                                 uint32_t bar, bool mn, int32_t r0, int32_t k0) {
   if (!mn) {
     tma_load_2d_pair(dst, map, bar, k0, r0);
   } else {
-    tma_load_2d_pair(dst, map, bar, r0, k0);
-    tma_load_2d_pair(dst + DBOX, map, bar, r0 + 64, k0);
+#pragma unroll
+    for (int r = 0; r < ROWS; r += 64)
+      tma_load_2d_pair(dst + r / 64 * DBOX, map, bar, r0 + r, k0);
   }
 }
 
@@ -414,23 +426,27 @@ __device__ __forceinline__ void pair_tile(int64_t t, int tiles_m, int tiles_n, i
   bj = r / rows;
 }
 
-template <bool GATED, int ACT, bool A_MN, bool B_MN, int S>
+template <bool GATED, int ACT, bool A_MN, bool B_MN, int S, int NB>
 __global__ void __launch_bounds__(PTHREADS, 1)
     dense_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmA2,
                       const __grid_constant__ CUtensorMap tmB2,
                       const __grid_constant__ OutMaps out, const DenseP p) {
-  constexpr int NT = GATED ? 128 : 256;   // columns of the output per tile
+  using C = Pair<NB>;
+  constexpr int NT = GATED ? NB / 2 : NB;   // columns of the output per tile
+  constexpr int PSTAGES = C::STAGES, PSTAGE = C::STAGE;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  PairCtl *ctl = reinterpret_cast<PairCtl *>(smem + PSTAGES * PSTAGE + 16 * PSLOT);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto *ctl = reinterpret_cast<PairCtl<PSTAGES> *>(smem + PSTAGES * PSTAGE + 16 * PSLOT);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr bool SPLIT = S > 1;           // S pairs in the cluster
-  const int crank = static_cast<int>(cluster_ctarank());
+  // (broadcasts tell the compiler that the values are the same in a warp)
+  const int crank = __shfl_sync(0xffffffffu, static_cast<int>(cluster_ctarank()), 0);
   const int rank = crank & 1, part = SPLIT ? crank >> 1 : 0, leader = crank & ~1;
-  const int64_t cluster = cluster_id_x(), clusters = gridDim.x / (2 * S);
+  const int64_t cluster = __shfl_sync(0xffffffffu, static_cast<int>(cluster_id_x()), 0);
+  const int64_t clusters = gridDim.x / (2 * S);
   const int tiles_n = static_cast<int>((p.N + NT - 1) / NT);
   const int64_t tiles = int64_t(p.tiles_m) * tiles_n;
   const int nk_all = p.nk1 * p.nseg, kb = SPLIT ? nk_all * part / S : 0;
@@ -452,7 +468,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     prefetch_tmap(&tmB);
   }
   __syncthreads();
-  if (warp == 9) tmem_alloc_pair(&ctl->tmem_base, 512);
+  if (warp == 9) tmem_alloc_pair(&ctl->tmem_base, 2 * NB);
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   // ring position: slot s, and the parity of its current round
   uint32_t issued = 0;
   if (warp == 8) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t round = 0;
       bool ok = true;
@@ -473,7 +489,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         int64_t bi, bj;
         pair_tile(t, p.tiles_m, tiles_n, bi, bj);
         const int32_t m0 = static_cast<int32_t>(bi * 256 + 128 * rank);
-        const int32_t n0 = static_cast<int32_t>(bj * NT + (GATED ? 0 : 128 * rank));
+        const int32_t n0 = static_cast<int32_t>(bj * NT + (GATED ? 0 : NB / 2 * rank));
         for (int it = 0; it < nk; ++it) {
           if (round > 0 && !mbar_wait(&ctl->empty[s], (round - 1) & 1, abort)) {
             ok = false;
@@ -484,9 +500,9 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           const int32_t k0 = (second ? kb + it - p.nk1 : kb + it) * DBK;
           const uint32_t bar = full0 + s * 8;
           if (rank == 0) mbar_expect_tx(&ctl->full[s], 2 * PSTAGE);
-          load_panel_pair(st, second ? &tmA2 : &tmA, bar, A_MN, m0, k0);
-          load_panel_pair(st + DPANEL, (GATED ? rank != 0 : second) ? &tmB2 : &tmB, bar, B_MN, n0,
-                          k0);
+          load_panel_pair<128>(st, second ? &tmA2 : &tmA, bar, A_MN, m0, k0);
+          load_panel_pair<NB / 2>(st + DPANEL, (GATED ? rank != 0 : second) ? &tmB2 : &tmB, bar,
+                                  B_MN, n0, k0);
           ++issued;
           if (++s == PSTAGES) s = 0, ++round;
         }
@@ -496,17 +512,16 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         ok = mbar_wait(&ctl->empty[e % PSTAGES], (e / PSTAGES) & 1, abort);
     }
   } else if (warp == 9) {
-    if (rank == 0 && lane == 0) {
-      const uint32_t idesc = idesc_make(1, A_MN, B_MN, 256, 256);
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_make(1, A_MN, B_MN, 256, NB);
       // descriptors of slot 0's first step; others differ in the address field
       const uint32_t a0 = smem_u32(smem), b0 = a0 + DPANEL;
       const uint64_t da0 = A_MN ? sdesc_sw128(a0, DBOX, 1024) : sdesc_sw128(a0, 16, 1024);
       const uint64_t db0 = B_MN ? sdesc_sw128(b0, DBOX, 1024) : sdesc_sw128(b0, 16, 1024);
-      // A barrier wait behind a commit holds the thread until the MMAs before
-      // the commit are done (measured: 560 cycles a slab of 4 MMAs whatever
-      // their width, 512 without waits at 256 columns). So the next slab is
-      // looked for before this one's commit; only a slab that is late is
-      // waited for behind it.
+      // Measured per slab of four 256 x 128 MMAs (260 cycles of tensor work): 335
+      // cycles with the barrier wait between the slabs, 264 with the next slab's
+      // barrier tested before this one's MMAs, so that only a slab that is late is
+      // waited for.
       int s = 0, i = 0;
       uint32_t parity = 0;
       bool ok = true, landed = false;
@@ -520,13 +535,13 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           }
           tc_fence_after();
           const uint32_t at = s * (PSTAGE >> 4);
-#pragma unroll
-          for (int kk = 0; kk < DBK / 16; ++kk)
-            umma_bf16_pair(tbase + 256 * a, da0 + at + kk * (A_MN ? 128 : 2),
-                           db0 + at + kk * (B_MN ? 128 : 2), idesc, (it | kk) != 0);
           uint64_t *used = &ctl->empty[s];
           if (++s == PSTAGES) s = 0, parity ^= 1;
-          landed = mbar_test(&ctl->full[s], parity);
+          landed = mbar_try_wait(&ctl->full[s], parity);
+#pragma unroll
+          for (int kk = 0; kk < DBK / 16; ++kk)
+            umma_bf16_pair(tbase + NB * a, da0 + at + kk * (A_MN ? 128 : 2),
+                           db0 + at + kk * (B_MN ? 128 : 2), idesc, (it | kk) != 0);
           umma_commit_pair(used, leader);
         }
         if (ok) umma_commit_pair(&ctl->tfull[a], leader);
@@ -542,12 +557,12 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q) << 16);
       if (alive) {   // this CTA's part -> shared memory
         const int r = 32 * q + lane;
-        for (int c = 128 * half; c < 128 * half + 128; c += 32) {
+        for (int c = NB / 2 * half; c < NB / 2 * (half + 1); c += 32) {
           float v[32];
           tmem_ld32(tq + c, v);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4 *>(smem + r * 1024 + ((c / 4 + j) ^ (r & 7)) * 16) =
+            *reinterpret_cast<float4 *>(smem + r * (NB * 4) + ((c / 4 + j) ^ (r & 7)) * 16) =
                 make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         }
       }
@@ -559,7 +574,8 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       int64_t bi, bj;
       pair_tile(cluster, p.tiles_m, tiles_n, bi, bj);
       constexpr int WIDTH = NT / S, PER_ROW = WIDTH / 4, STEP = 32 / PER_ROW;
-      constexpr int U = GATED ? 8 / S : 16 / S;   // 16 remote loads in flight a lane
+      // up to 16 remote loads in flight a lane, and no row twice
+      constexpr int U = (GATED ? 8 : 16) / S < 16 / STEP ? (GATED ? 8 : 16) / S : 16 / STEP;
       const int cc = WIDTH * part + lane % PER_ROW * 4;
       const int64_t col = bj * NT + cc, row0 = bi * 256 + 128 * rank;
       const int n = static_cast<int>(kq_max<int64_t>(kq_min<int64_t>(4, p.N - col), 0));
@@ -578,9 +594,9 @@ __global__ void __launch_bounds__(PTHREADS, 1)
 #pragma unroll
           for (int k = 0; k < U; ++k) {
             const int r = kq_min(r0 + k * STEP, 127);
-            x[o][k] = ld_dsmem_f4(base[o] + r * 1024 + ((cc / 4) ^ (r & 7)) * 16);
+            x[o][k] = ld_dsmem_f4(base[o] + r * (NB * 4) + ((cc / 4) ^ (r & 7)) * 16);
             if constexpr (GATED)
-              y[o][k] = ld_dsmem_f4(base[o] + r * 1024 + ((cc / 4 + 32) ^ (r & 7)) * 16);
+              y[o][k] = ld_dsmem_f4(base[o] + r * (NB * 4) + ((cc / 4 + NB / 8) ^ (r & 7)) * 16);
           }
         }
 #pragma unroll
@@ -602,7 +618,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           if (GATED && p.Z) store4(p.Z2 + row * p.ldz + col, u, n);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            v[t] = act_f<ACT>(v[t]);
+            v[t] = act_run(p.act, v[t]);
             if (GATED) v[t] *= u[t];
             else if (p.R) v[t] += t < n ? __bfloat162float(p.R[row * p.ldr + col + t]) : 0.f;
           }
@@ -617,7 +633,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       int64_t bi, bj;
       pair_tile(t, p.tiles_m, tiles_n, bi, bj);
       const int64_t row0 = bi * 256 + 128 * rank + 32 * q;   // this warp's rows
-      const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q) << 16) + 256 * a;
+      const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q) << 16) + NB * a;
       // residual values of columns [col, col + 64) into a slot
       auto residual = [&](uint8_t *slot, int64_t col) {
 #pragma unroll
@@ -630,8 +646,12 @@ __global__ void __launch_bounds__(PTHREADS, 1)
                      bytes > 0 ? p.R + row * p.ldr + c : p.R, bytes);
         }
       };
-      const int first = half * (NT / 2);
-      const bool early = !GATED && p.R && !p.Z;   // the first output takes R
+      // columns of this half: NT / 2, or, where that is less than a slot, all of
+      // them for the first half
+      constexpr int MINE = NT >= 128 ? NT / 128 : 1;
+      const bool busy = NT >= 128 || half == 0;
+      const int first = NT >= 128 ? half * (NT / 2) : 0;
+      const bool early = !GATED && busy && p.R && !p.Z;   // the first output takes R
       if (early) {
         slot_free<false>(lane);
         residual(slots + (used & 1) * PSLOT, bj * NT + first);
@@ -639,7 +659,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       const bool ok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      for (int c = 0; c < NT / 128; ++c) {
+      for (int c = 0; c < MINE && busy; ++c) {
         const int cc = first + 64 * c;
         const int64_t col = bj * NT + cc;
         if (col >= p.N || row0 >= p.M) break;
@@ -651,7 +671,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               float v[32];
-              tmem_ld32(tq + cc + 128 * o + 32 * h, v);
+              tmem_ld32(tq + cc + NB / 2 * o + 32 * h, v);
               if (!GATED && p.bias) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
@@ -671,7 +691,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         for (int h = 0; h < 2; ++h) {
           float v[32], u[GATED ? 32 : 1];
           tmem_ld32(tq + cc + 32 * h, v);
-          if constexpr (GATED) tmem_ld32(tq + cc + 128 + 32 * h, u);
+          if constexpr (GATED) tmem_ld32(tq + cc + NB / 2 + 32 * h, u);
           if (!GATED && p.bias) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
@@ -711,7 +731,8 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   __syncthreads();
   if (ctl->abort) {
     if (threadIdx.x == 0) report(p.info, KRONQ_ERR_TIMEOUT);
-    if (rank == 0 && warp == 8 && lane == 0) {
+    // (the same lanes are elected again)
+    if (rank == 0 && warp == 8 && elect_one()) {
       const uint64_t t0 = globaltimer();
       for (uint32_t s = 0; s < PSTAGES && s < issued; ++s) {
         const uint32_t last = ((issued - 1 - s) / PSTAGES) * PSTAGES + s;
@@ -720,7 +741,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         }
       }
     }
-    if (rank == 0 && warp == 9 && lane == 0) {
+    if (rank == 0 && warp == 9 && elect_one()) {
       umma_commit_pair(&ctl->drain, leader);
       const uint64_t t0 = globaltimer();
       while (!mbar_try_wait(&ctl->drain, 0) && globaltimer() - t0 < kWaitLimitNs) {
@@ -731,7 +752,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   cluster_sync_all();
   if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc_pair(tbase, 512);
+    tmem_dealloc_pair(tbase, 2 * NB);
   }
 }
 
@@ -898,9 +919,9 @@ kronq_status with_act(int act, F f) {
 
 // rows x K operand: K-major maps are {K, rows}, MN-major ones {rows, K}
 kronq_status operand_map(CUtensorMap *m, const void *p, int64_t ld, bool mn, int64_t rows,
-                         int64_t K) {
+                         int64_t K, int box_rows) {
   return mn ? make_tmap_2d(m, p, true, rows, K, ld, 64, DBK)
-            : make_tmap_2d(m, p, true, K, rows, ld, DBK, DT);
+            : make_tmap_2d(m, p, true, K, rows, ld, DBK, box_rows);
 }
 
 // How a product is launched: the few-token kernel splits k over `split` CTAs
@@ -923,31 +944,72 @@ kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d,
                        tm[2], tm[3], p);
 }
 
-template <bool GATED, int ACT, bool A_MN, bool B_MN>
-kronq_status launch_pair(cudaStream_t st, const CUtensorMap *tm, DenseP p) {
-  p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
-  const int64_t tiles = p.tiles_m * ceil_div(p.N, GATED ? 128 : 256);
-  const int nk = p.nk1 * p.nseg;
+// How a product runs on pairs: columns of the accumulator and pairs a tile.
+//   A round of 74 pairs takes about nk * 520 + 6000 cycles at 256 columns and
+// nk * 320 + 5000 at 128 (nk slabs of k). Where a single round leaves pairs idle, k is
+// split over two or four of them if the clusters that takes all fit on the chip
+// (33 of four CTAs of this size, 15 of eight) and at least 8 slabs remain each.
+struct PairPlan {
+  int nb, split;
+};
+PairPlan pair_plan(int64_t rows, int64_t cols, int nk, bool gated) {
+  const int64_t tm = ceil_div(rows, 256);
+  const int64_t wide = tm * ceil_div(cols, gated ? 128 : 256);
+  const int64_t narrow = tm * ceil_div(cols, gated ? 64 : 128);
+  if (narrow <= 15 && nk >= 32) return {128, 4};
+  if (narrow <= 33 && nk >= 16) return {128, 2};
+  const int64_t c256 = ceil_div(wide, 74) * (int64_t(nk) * 520 + 6000);
+  const int64_t c128 = ceil_div(narrow, 74) * (int64_t(nk) * 320 + 5000);
+  return {c128 < c256 ? 128 : 256, 1};
+}
+
+struct Operands {
+  Mat X, W, X2, W2;
+};
+
+// D (M x N) = A B^T on pairs, A = (o.X, o.X2), B = (o.W, o.W2)
+template <bool GATED, bool A_MN, bool B_MN>
+kronq_status launch_pair(cudaStream_t st, const Operands &o, DenseP p, int act) {
+  const PairPlan plan = pair_plan(p.M, p.N, p.nk1 * p.nseg, GATED);
+  CUtensorMap tm[4];
+  memset(tm, 0, sizeof(tm));
+  KQ_TRY(operand_map(&tm[0], o.X.p, o.X.ld, A_MN, p.M, p.K, 128));
+  KQ_TRY(operand_map(&tm[1], o.W.p, o.W.ld, B_MN, p.N, p.K, plan.nb / 2));
+  if (o.X2.p) KQ_TRY(operand_map(&tm[2], o.X2.p, o.X2.ld, A_MN, p.M, p.K, 128));
+  if (o.W2.p) KQ_TRY(operand_map(&tm[3], o.W2.p, o.W2.ld, B_MN, p.N, p.K, plan.nb / 2));
   OutMaps out;
   memset(&out, 0, sizeof(out));
   const int64_t n8 = p.N & ~int64_t(7);
-  if (n8) KQ_TRY(make_tmap_2d(&out.y, p.Y, true, n8, p.M, p.ldy, 64, 32));
-  if (n8 && p.Z) KQ_TRY(make_tmap_2d(&out.z, p.Z, true, n8, p.M, p.ldz, 64, 32));
-  if (n8 && p.Z2) KQ_TRY(make_tmap_2d(&out.z2, p.Z2, true, n8, p.M, p.ldz, 64, 32));
-  auto split = [&](auto s) {
-    constexpr int S = decltype(s)::value;
-    auto *kern = dense_pair_kernel<GATED, ACT, A_MN, B_MN, S>;
-    KQ_TRY(smem_attr(kern, PSMEM));
-    return launch_kernel(st, kern, tiles * 2 * S, PTHREADS, PSMEM, 2 * S, true, tm[0], tm[1],
-                         tm[2], tm[3], out, p);
+  if (n8 && plan.split == 1) {
+    KQ_TRY(make_tmap_2d(&out.y, p.Y, true, n8, p.M, p.ldy, 64, 32));
+    if (p.Z) KQ_TRY(make_tmap_2d(&out.z, p.Z, true, n8, p.M, p.ldz, 64, 32));
+    if (p.Z2) KQ_TRY(make_tmap_2d(&out.z2, p.Z2, true, n8, p.M, p.ldz, 64, 32));
+  }
+  p.act = act;
+  p.tiles_m = static_cast<int>(ceil_div(p.M, 256));
+  auto go = [&](auto a, auto split, auto nb) {
+    constexpr int S = decltype(split)::value, NB = decltype(nb)::value;
+    auto *kern = dense_pair_kernel<GATED, decltype(a)::value, A_MN, B_MN, S, NB>;
+    KQ_TRY(smem_attr(kern, Pair<NB>::SMEM));
+    const int64_t tiles = p.tiles_m * ceil_div(p.N, GATED ? NB / 2 : NB);
+    return launch_kernel(st, kern, 2 * S * (S > 1 ? tiles : kq_min<int64_t>(tiles, 74)), PTHREADS,
+                         Pair<NB>::SMEM, 2 * S, true, tm[0], tm[1], tm[2], tm[3], out, p);
   };
-  // clusters of 8 CTAs of this size: 15 fit on the chip at once, of 4: 33
-  if (!GATED && tiles <= 15 && nk >= 16) return split(std::integral_constant<int, GATED ? 2 : 4>());
-  if (tiles <= 33 && nk >= 8) return split(std::integral_constant<int, 2>());
-  auto *kern = dense_pair_kernel<GATED, ACT, A_MN, B_MN, 1>;
-  KQ_TRY(smem_attr(kern, PSMEM));
-  return launch_kernel(st, kern, 2 * kq_min<int64_t>(tiles, 74), PTHREADS, PSMEM, 2, true, tm[0],
-                       tm[1], tm[2], tm[3], out, p);
+  using I0 = std::integral_constant<int, KRONQ_ACT_NONE>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I4 = std::integral_constant<int, 4>;
+  using N128 = std::integral_constant<int, 128>;
+  using N256 = std::integral_constant<int, 256>;
+  if (plan.split == 4) return go(I0(), I4(), N128());   // (split tiles: p.act)
+  if (plan.split == 2) return go(I0(), I2(), N128());
+  if constexpr (!A_MN && !B_MN) {
+    return with_act(act, [&](auto a) {
+      return plan.nb == 128 ? go(a, I1(), N128()) : go(a, I1(), N256());
+    });
+  } else {
+    return plan.nb == 128 ? go(I0(), I1(), N128()) : go(I0(), I1(), N256());
+  }
 }
 
 // Tokens per tile of the few-token kernel, 0 for the pair kernel.
@@ -955,34 +1017,22 @@ int few_width(int64_t tokens) {
   return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 0;
 }
 
-// Tensor maps of D = X W^T by the kernel that takes it: panels of the token
-// operand are NT rows (few) or 128 rows.
-struct Operands {
-  Mat X, W, X2, W2;
-};
+// D = X W^T by the kernel that takes it: few tokens, or pairs
 template <bool GATED, bool W_MN>
 kronq_status tokens_product(cudaStream_t st, const Operands &o, const DenseP &p, int act) {
-  const int64_t K = p.K;
   const int nt = few_width(p.M);
+  if (nt == 0) return launch_pair<GATED, false, W_MN>(st, o, p, act);
   CUtensorMap tm[4];
   memset(tm, 0, sizeof(tm));
-  const uint32_t box = nt ? nt : DT;
-  KQ_TRY(make_tmap_2d(&tm[0], o.X.p, true, K, p.M, o.X.ld, DBK, box));
-  KQ_TRY(operand_map(&tm[1], o.W.p, o.W.ld, W_MN, p.N, K));
-  if (o.X2.p) KQ_TRY(make_tmap_2d(&tm[2], o.X2.p, true, K, p.M, o.X2.ld, DBK, box));
-  if (o.W2.p) KQ_TRY(operand_map(&tm[3], o.W2.p, o.W2.ld, W_MN, p.N, K));
+  KQ_TRY(operand_map(&tm[0], o.X.p, o.X.ld, false, p.M, p.K, nt));
+  KQ_TRY(operand_map(&tm[1], o.W.p, o.W.ld, W_MN, p.N, p.K, DT));
+  if (o.X2.p) KQ_TRY(operand_map(&tm[2], o.X2.p, o.X2.ld, false, p.M, p.K, nt));
+  if (o.W2.p) KQ_TRY(operand_map(&tm[3], o.W2.p, o.W2.ld, W_MN, p.N, p.K, DT));
   switch (nt) {
     case 16: return launch_few<GATED, W_MN, 16>(st, tm, p, act);
     case 32: return launch_few<GATED, W_MN, 32>(st, tm, p, act);
     case 64: return launch_few<GATED, W_MN, 64>(st, tm, p, act);
-    case 128: return launch_few<GATED, W_MN, 128>(st, tm, p, act);
-  }
-  if constexpr (W_MN) {
-    return launch_pair<false, KRONQ_ACT_NONE, false, true>(st, tm, p);
-  } else {
-    return with_act(act, [&](auto a) {
-      return launch_pair<GATED, decltype(a)::value, false, false>(st, tm, p);
-    });
+    default: return launch_few<GATED, W_MN, 128>(st, tm, p, act);
   }
 }
 
@@ -1006,10 +1056,6 @@ kronq_status input_grad(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out,
 // dW = G^T X
 kronq_status weight_grad(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out, const Mat &G,
                          const Mat &X, const Mat &dW, int32_t *info) {
-  CUtensorMap tm[4];
-  memset(tm, 0, sizeof(tm));
-  KQ_TRY(operand_map(&tm[0], G.p, G.ld, true, d_out, n));
-  KQ_TRY(operand_map(&tm[1], X.p, X.ld, true, d_in, n));
   DenseP p = {};
   p.M = d_out;
   p.N = d_in;
@@ -1019,7 +1065,7 @@ kronq_status weight_grad(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out
   p.Y = static_cast<__nv_bfloat16 *>(dW.p);
   p.ldy = dW.ld;
   p.info = info;
-  return launch_pair<false, KRONQ_ACT_NONE, true, true>(st, tm, p);
+  return launch_pair<false, true, true>(st, Operands{G, X, Mat{}, Mat{}}, p, KRONQ_ACT_NONE);
 }
 
 kronq_status zero_rows(cudaStream_t st, const Mat &m, int64_t rows, int64_t cols) {
