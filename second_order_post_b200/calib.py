@@ -1,0 +1,119 @@
+"""The calibration pass of one gated feed-forward block, from its input tokens
+to the covariances that the quantizer takes [gptget-en Methodology: H_G from
+one backward pass; wmrh §二].
+
+``FeedForwardCalibration`` holds the block's weights (gate, up, down, and the
+head that turns its output into logits) and the buffers of one batch of
+tokens, and enqueues on one CUDA stream, per batch:
+
+  forward   H = act(X Wgᵀ) * (X Wuᵀ)             kronq_gated
+            Y = H Wdᵀ + X                        kronq_linear (residual stream)
+            logits = Y Whᵀ                       kronq_linear
+  loss      distillation from the teacher's top logits, and its gradient
+                                                 kronq_distill_step (in place)
+  backward  dY = dlogits Wh                      kronq_linear_bwd
+            dH = dY Wd                           kronq_linear_bwd
+            Gg, Gu, dX = ... + dY                kronq_gated_bwd
+  sums      H_X of gate/up (X) and of down (H), H_G of gate (Gg), up (Gu) and
+            down (dY)                            kronq_accum_cov
+
+The weights are not updated: no weight gradient is formed. All arithmetic runs
+in the library's kernels; this module only allocates and passes pointers.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import kronq as K
+
+SUBLAYERS = ("gate", "up", "down")
+
+
+class FeedForwardCalibration:
+    def __init__(self, Wg, Wu, Wd, Wh, max_tokens, tokens, act="silu", tau=1.0):
+        """bf16 CUDA weights Wg, Wu (f x d), Wd (d x f), Wh (vocab x d), with d
+        and f multiples of 128 (the covariances' rule); `max_tokens`: the largest
+        batch; `tokens`: how many tokens the covariances are normalised by
+        (those of all batches)."""
+        f, d = Wg.shape
+        if Wu.shape != (f, d) or Wd.shape != (d, f) or Wh.shape[1] != d:
+            raise ValueError("the weights do not belong to one block")
+        if d % 128 or f % 128:
+            raise ValueError("the block's widths must be multiples of 128")
+        if max_tokens < 1 or tokens < 1:
+            raise ValueError("max_tokens and tokens must be positive")
+        self.Wg, self.Wu, self.Wd, self.Wh = Wg, Wu, Wd, Wh
+        self.act, self.tau, self.tokens = K.KRONQ_ACTS[act], float(tau), int(tokens)
+        self.max_tokens = int(max_tokens)
+        dev, n, vocab = Wg.device, self.max_tokens, Wh.shape[0]
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self._act = {name: torch.empty(n, f, **bf) for name in ("A", "U", "H", "dH")}
+        self._res = {name: torch.empty(n, d, **bf) for name in ("Y", "dY", "dX")}
+        # rows of logits start on 16-byte boundaries, as kronq_linear wants them
+        self._logits = torch.empty(n, (vocab + 7) // 8 * 8, **bf)[:, :vocab]
+        self._loss = torch.empty(n, **f32)
+        self.H_X = {"mlp": torch.empty(d, d, **f32), "down": torch.empty(f, f, **f32)}
+        self.H_G = {"gate": torch.empty(f, f, **f32), "up": torch.empty(f, f, **f32),
+                    "down": torch.empty(d, d, **f32)}
+        # status words: the block's products and loss (written on failure only,
+        # cleared here), then the five covariances
+        self.info = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.cov_info = torch.zeros(5, dtype=torch.int32, device=dev)
+        self._first = True
+
+    def step(self, X, T, idx, weight=None, stream=None):
+        """One batch: X (n x d bf16 tokens), the teacher's top logits T and
+        their places idx (n x k), weight (n fp32, None: all 1). Returns the
+        tokens' losses and dX, the gradient with respect to X (views that the
+        next step overwrites)."""
+        n = X.shape[0]
+        if not 1 <= n <= self.max_tokens:
+            raise ValueError(f"a batch has 1 to {self.max_tokens} tokens, not {n}")
+        A, U, H, dH = (self._act[k][:n] for k in ("A", "U", "H", "dH"))
+        Y, dY, dX = (self._res[k][:n] for k in ("Y", "dY", "dX"))
+        logits, loss, info = self._logits[:n], self._loss[:n], self.info
+        K.kronq_gated(X, self.Wg, self.Wu, H, info, act=self.act, A=A, U=U, stream=stream)
+        K.kronq_linear(H, self.Wd, Y, info, R=X, stream=stream)
+        K.kronq_linear(Y, self.Wh, logits, info, stream=stream)
+        K.kronq_distill_step(logits, T, idx, loss, None, logits, info, tau=self.tau,
+                             weight=weight, stream=stream)
+        K.kronq_linear_bwd(logits, None, self.Wh, info, dX=dY, stream=stream)
+        K.kronq_linear_bwd(dY, None, self.Wd, info, dX=dH, stream=stream)
+        # Gg and Gu take the place of A and U
+        K.kronq_gated_bwd(dH, A, U, None, self.Wg, self.Wu, A, U, info, act=self.act, dX=dX,
+                          dXr=dY, stream=stream)
+        beta = 0.0 if self._first else 1.0
+        self._first = False
+        sums = ((X, self.H_X["mlp"]), (H, self.H_X["down"]), (A, self.H_G["gate"]),
+                (U, self.H_G["up"]), (dY, self.H_G["down"]))
+        for i, (rows, cov) in enumerate(sums):
+            K.kronq_accum_cov(rows, cov, 1.0 / self.tokens, beta, self.cov_info[i:i + 1], stream)
+        return loss, dX
+
+    def covariances(self, sublayer):
+        """(H_X, H_G) of "gate", "up" or "down"."""
+        if sublayer not in SUBLAYERS:
+            raise ValueError(f"sublayer must be one of {SUBLAYERS}")
+        return self.H_X["down" if sublayer == "down" else "mlp"], self.H_G[sublayer]
+
+    def weight(self, sublayer):
+        return {"gate": self.Wg, "up": self.Wu, "down": self.Wd}[sublayer]
+
+    def quantize(self, sublayer, engine, stream=None):
+        """BiIP, factor and OBS of one sublayer on copies of its covariances, in
+        a SublayerEngine of its shape; returns the engine's QuantResult."""
+        hx, hg = self.covariances(sublayer)
+        with torch.cuda.stream(stream or torch.cuda.current_stream(hx.device)):
+            engine.H_X.copy_(hx)
+            engine.H_G.copy_(hg)
+        return engine.run_from_covariances(self.weight(sublayer), stream)
+
+    def check_info(self):
+        """Raises KronqError for a status word that is not 0 (syncs)."""
+        v = int(self.info.item())
+        if v:
+            raise K.KronqError("kronq calibration pass", v & 0xFF)
+        for v in self.cov_info.tolist():
+            if v:
+                raise K.KronqError("kronq_accum_cov", v & 0xFF)

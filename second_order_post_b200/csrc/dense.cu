@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const ActBwdP p) {
 // shared memory). Bound by reading dY and Z and writing dZ once.
 constexpr int BG_MAXC = 8;
 template <int ACT>
-__global__ void __launch_bounds__(256) bias_grad_kernel(const ActBwdP p, float *db, int parts) {
+__global__ void __launch_bounds__(256, 4) bias_grad_kernel(const ActBwdP p, float *db, int parts) {
   __shared__ __align__(16) float part[32][64];
   const int cg = threadIdx.x & 7, rl = threadIdx.x >> 3;
   const int rank = blockIdx.x % parts;
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(const ActBwdP p, float *
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (n > 0) {
     const int64_t step = 32 * parts;
-    constexpr int U = 4;   // rows in flight
+    constexpr int U = 2;   // rows in flight (64 registers: four CTAs an SM, one wave)
     for (int64_t r0 = rank * 32 + rl; r0 < p.n; r0 += U * step) {
       float g[U][8], z[U][8];
 #pragma unroll

@@ -14,6 +14,12 @@ chol    kronq_chol_inv on a d x d symmetric positive definite matrix
 quant   kronq_chol_inv, then kronq_quantize_sublayer of a d x d weight
         (N(0, 0.02^2)) at 2 bits
 
+linear  kronq_linear of --n tokens through a --d-out x --d sublayer with residual,
+        then its kronq_linear_bwd (input and weight gradients)
+gated   kronq_gated of --n tokens through a pair of --d-out x --d projections, then
+        its kronq_gated_bwd (input gradient)
+distill kronq_distill_step of --n rows of --d-out bf16 logits, 64 teacher logits each
+
 Every call goes through the C ABI; the status words are checked at the end.
 With --time, each call after the first is timed with CUDA events (L2 flushed
 by a 512 MB write before it) and the median is printed in ms.
@@ -142,23 +148,83 @@ def run_quant(args):
     return [eng.info[3].item(), eng.info[4].item()]
 
 
+def _bf16(rows, cols, gen, scale=1.0):
+    return (torch.randn(rows, cols, generator=gen, device="cuda") * scale).to(torch.bfloat16)
+
+
+def run_linear(args):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    X, W = _bf16(args.n, args.d, g), _bf16(args.d_out, args.d, g, args.d ** -0.5)
+    R, dY = _bf16(args.n, args.d_out, g), _bf16(args.n, args.d_out, g, 1e-3)
+    Y, dX, dW = torch.empty_like(R), torch.empty_like(X), torch.empty_like(W)
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step():
+        K.kronq_linear(X, W, Y, info, R=R)
+        K.kronq_linear_bwd(dY, X, W, info, dX=dX, dW=dW)
+    for r in range(args.reps):
+        args.timer(step, r == 0)
+    torch.cuda.synchronize()
+    return [info.item()]
+
+
+def run_gated(args):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    X = _bf16(args.n, args.d, g)
+    Wg, Wu = (_bf16(args.d_out, args.d, g, args.d ** -0.5) for _ in range(2))
+    dH = _bf16(args.n, args.d_out, g, 1e-3)
+    H, A, U = (torch.empty_like(dH) for _ in range(3))
+    dX = torch.empty_like(X)
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step():
+        K.kronq_gated(X, Wg, Wu, H, info, A=A, U=U)
+        K.kronq_gated_bwd(dH, A, U, None, Wg, Wu, A, U, info, dX=dX)
+    for r in range(args.reps):
+        args.timer(step, r == 0)
+    torch.cuda.synchronize()
+    return [info.item()]
+
+
+def run_distill(args):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    Z = torch.randn(args.n, args.d_out, generator=g, device="cuda") * 2.5
+    top = (Z + torch.randn(args.n, args.d_out, generator=g, device="cuda")).topk(64, dim=1)
+    Z, T, idx = Z.to(torch.bfloat16), top.values.contiguous(), top.indices.int().contiguous()
+    loss, dZ = torch.empty(args.n, device="cuda"), torch.empty_like(Z)
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for r in range(args.reps):
+        args.timer(lambda: K.kronq_distill_step(Z, T, idx, loss, None, dZ, info, tau=2.0), r == 0)
+    torch.cuda.synchronize()
+    return [info.item()]
+
+
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("step", choices=["cov", "biip", "matvec", "chol", "quant"])
+    ap.add_argument("step", choices=["cov", "biip", "matvec", "chol", "quant", "linear", "gated",
+                                     "distill"])
     ap.add_argument("--d", type=int, default=28672)
     ap.add_argument("--n", type=int, default=16384)
+    ap.add_argument("--d-out", type=int, default=11008)
     ap.add_argument("--workload", default="llama3_70b_down_8192x28672")
     ap.add_argument("--reps", type=int, default=2)
     ap.add_argument("--time", action="store_true")
     args = ap.parse_args()
     args.timer = _Timer(args.time)
     info = {"cov": run_cov, "biip": run_biip, "matvec": run_matvec, "chol": run_chol,
-            "quant": run_quant}[args.step](args)
+            "quant": run_quant, "linear": run_linear, "gated": run_gated,
+            "distill": run_distill}[args.step](args)
     if any(info):
         raise SystemExit(f"status word(s) {info}")
     print(f"{args.step} ok")
     if args.time and args.timer.ms:
         shape = ({"workload": args.workload} if args.step in ("biip", "matvec")
+                 else {"n": args.n, "vocab": args.d_out} if args.step == "distill"
+                 else {"n": args.n, "d": args.d, "d_out": args.d_out}
+                 if args.step in ("linear", "gated")
                  else {"d": args.d, **({"n": args.n} if args.step == "cov" else {})})
         print(json.dumps({"step": args.step, **shape,
                           "ms_median": statistics.median(args.timer.ms),
