@@ -27,16 +27,24 @@ __device__ __forceinline__ float act_f(float z) {
   return z;
 }
 
-// the same with the activation chosen at run time
-__device__ __forceinline__ float act_run(int act, float z) {
+// Four values, the activation chosen at run time. Not inlined: a tile's epilogue
+// runs once or a few times, so what it costs is fetching its code, and unrolled
+// copies of five activations took longer to fetch (8000 cycles a tile) than
+// the tile took to multiply.
+template <int ACT>
+__device__ __forceinline__ float4 act4_f(float4 z) {
+  return make_float4(act_f<ACT>(z.x), act_f<ACT>(z.y), act_f<ACT>(z.z), act_f<ACT>(z.w));
+}
+static __device__ __noinline__ float4 act4(int act, float4 z) {
   switch (act) {
-    case KRONQ_ACT_RELU: return act_f<KRONQ_ACT_RELU>(z);
-    case KRONQ_ACT_SILU: return act_f<KRONQ_ACT_SILU>(z);
-    case KRONQ_ACT_GELU: return act_f<KRONQ_ACT_GELU>(z);
-    case KRONQ_ACT_GELU_TANH: return act_f<KRONQ_ACT_GELU_TANH>(z);
+    case KRONQ_ACT_RELU: return act4_f<KRONQ_ACT_RELU>(z);
+    case KRONQ_ACT_SILU: return act4_f<KRONQ_ACT_SILU>(z);
+    case KRONQ_ACT_GELU: return act4_f<KRONQ_ACT_GELU>(z);
+    case KRONQ_ACT_GELU_TANH: return act4_f<KRONQ_ACT_GELU_TANH>(z);
     default: return z;
   }
 }
+static __device__ __noinline__ float4 gelu4(float4 z) { return act4_f<KRONQ_ACT_GELU>(z); }
 
 // value and derivative
 template <int ACT>

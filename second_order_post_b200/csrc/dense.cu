@@ -75,7 +75,7 @@ struct Few {
 
 struct FewP {
   DenseP d;
-  int act, split, tiles_t;   // CTAs per tile, token tiles
+  int split, tiles_t;   // CTAs per tile, token tiles
 };
 
 template <int STAGES>
@@ -85,15 +85,37 @@ struct FewCtl {
   int abort;
 };
 
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *v, int n) {
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v, int n) {
+  const __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
   if (n >= 4) {
-    __nv_bfloat162 o[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
     *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(o);
   } else {
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      if (t < n) p[t] = __float2bfloat16_rn(v[t]);
+    p[0] = o[0].x;
+    if (n > 1) p[1] = o[0].y;
+    if (n > 2) p[2] = o[1].x;
   }
+}
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+// The epilogue of four consecutive columns (n of them in range) of a row, bias
+// added: v the accumulator (gated: v of the gate, u of the up projection).
+template <bool GATED>
+__device__ __forceinline__ void finish4(const DenseP &p, int64_t row, int64_t col, int n, float4 v,
+                                        float4 u) {
+  if (p.Z) store4(p.Z + row * p.ldz + col, v, n);
+  if (GATED && p.Z) store4(p.Z2 + row * p.ldz + col, u, n);
+  if (p.act != KRONQ_ACT_NONE) v = act4(p.act, v);
+  if (GATED) {
+    v = make_float4(v.x * u.x, v.y * u.y, v.z * u.z, v.w * u.w);
+  } else if (p.R) {
+    const __nv_bfloat16 *r = p.R + row * p.ldr + col;
+    v.x += __bfloat162float(r[0]);
+    if (n > 1) v.y += __bfloat162float(r[1]);
+    if (n > 2) v.z += __bfloat162float(r[2]);
+    if (n > 3) v.w += __bfloat162float(r[3]);
+  }
+  store4(p.Y + row * p.ldy + col, v, n);
 }
 
 template <bool GATED, bool W_MN, int NT>
@@ -219,44 +241,55 @@ __global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
   if (split > 1) cluster_sync_all();
   else __syncthreads();
 
-  // ---- sum over the parts, epilogue: four features of a token per step
+  // ---- sum over the parts, epilogue: four features of a token per step, every
+  // part's loads of U steps in flight together
   const int tokens = static_cast<int>(kq_min<int64_t>(NT, p.M - t0));
-  uint32_t addr[8];
-#pragma unroll
-  for (int r = 0; r < 8; ++r)
-    addr[r] = split > 1 && r < split ? mapa_shared(smem_u32(part), r) : smem_u32(part);
+  const int items = tokens * (DT / 4), stride = split * FTHREADS;
+  constexpr int U = NT <= 32 ? 1 : 2;
   if (!*abort) {
-    for (int e = rank * FTHREADS + threadIdx.x; e < tokens * (DT / 4); e += split * FTHREADS) {
-      const int t = e / (DT / 4), c = e % (DT / 4) * 4;
-      const int64_t col = f0 + c, row = t0 + t;
-      if (col >= p.N) continue;
-      const int n = static_cast<int>(kq_min<int64_t>(4, p.N - col));
-      float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int e0 = rank * FTHREADS + threadIdx.x; e0 < items; e0 += U * stride) {
+      float4 v[U], u[U];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        if (r < split) {
-          const uint32_t at = addr[r] + static_cast<uint32_t>(t * DT + c) * 4;
-          const float4 x = ld_dsmem_f4(at);
-          v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-          if (GATED) {
-            const float4 y = ld_dsmem_f4(at + NT * DT * 4);
-            u[0] += y.x; u[1] += y.y; u[2] += y.z; u[3] += y.w;
+      for (int k = 0; k < U; ++k) v[k] = u[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r0 = 0; r0 < split; r0 += 4) {   // four parts at a time
+        float4 x[4][U], y[4][GATED ? U : 1];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int o = kq_min(r0 + r, split - 1);
+          const uint32_t base = split > 1 ? mapa_shared(smem_u32(part), o) : smem_u32(part);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int e = kq_min(e0 + k * stride, items - 1);   // (token, features) e
+            x[r][k] = ld_dsmem_f4(base + static_cast<uint32_t>(e) * 16);
+            if constexpr (GATED)
+              y[r][k] = ld_dsmem_f4(base + static_cast<uint32_t>(e) * 16 + NT * DT * 4);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            v[k] = add4(v[k], r0 + r < split ? x[r][k] : zero);
+            if constexpr (GATED) u[k] = add4(u[k], r0 + r < split ? y[r][k] : zero);
           }
         }
       }
-      if (!GATED && p.bias) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] += k < n ? __ldg(p.bias + col + k) : 0.f;
+      for (int k = 0; k < U; ++k) {
+        const int e = e0 + k * stride, t = e / (DT / 4);
+        const int64_t col = f0 + e % (DT / 4) * 4;
+        if (e >= items || col >= p.N) continue;
+        const int n = static_cast<int>(kq_min<int64_t>(4, p.N - col));
+        if (!GATED && p.bias) {
+          v[k].x += p.bias[col];
+          if (n > 1) v[k].y += p.bias[col + 1];
+          if (n > 2) v[k].z += p.bias[col + 2];
+          if (n > 3) v[k].w += p.bias[col + 3];
+        }
+        finish4<GATED>(p, t0 + t, col, n, v[k], u[k]);
       }
-      if (p.Z) store4(p.Z + row * p.ldz + col, v, n);
-      if (GATED && p.Z) store4(p.Z2 + row * p.ldz + col, u, n);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        v[k] = act_run(fp.act, v[k]);
-        if (GATED) v[k] *= u[k];
-        else if (p.R) v[k] += k < n ? __bfloat162float(p.R[row * p.ldr + col + k]) : 0.f;
-      }
-      store4(p.Y + row * p.ldy + col, v, n);
     }
   }
   // no CTA leaves while another may still read its part
@@ -574,29 +607,31 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       int64_t bi, bj;
       pair_tile(cluster, p.tiles_m, tiles_n, bi, bj);
       constexpr int WIDTH = NT / S, PER_ROW = WIDTH / 4, STEP = 32 / PER_ROW;
-      // up to 16 remote loads in flight a lane, and no row twice
-      constexpr int U = (GATED ? 8 : 16) / S < 16 / STEP ? (GATED ? 8 : 16) / S : 16 / STEP;
+      // rows in flight: up to 8 loads a lane
+      constexpr int U = 8 / (S * (GATED ? 2 : 1)) < 16 / STEP ? 8 / (S * (GATED ? 2 : 1)) : 16 / STEP;
       const int cc = WIDTH * part + lane % PER_ROW * 4;
       const int64_t col = bj * NT + cc, row0 = bi * 256 + 128 * rank;
       const int n = static_cast<int>(kq_max<int64_t>(kq_min<int64_t>(4, p.N - col), 0));
-      float bias[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) bias[k] = !GATED && p.bias && k < n ? p.bias[col + k] : 0.f;
-      uint32_t base[S];
-#pragma unroll
-      for (int o = 0; o < S; ++o) base[o] = mapa_shared(smem_u32(smem), 2 * o + rank);
+      float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!GATED && p.bias && n > 0) {
+        bias.x = p.bias[col];
+        if (n > 1) bias.y = p.bias[col + 1];
+        if (n > 2) bias.z = p.bias[col + 2];
+        if (n > 3) bias.w = p.bias[col + 3];
+      }
 #pragma unroll 1
       for (int r0 = warp * 16 + lane / PER_ROW; r0 < warp * 16 + 16 && alive && n > 0;
            r0 += U * STEP) {
         float4 x[S][U], y[S][GATED ? U : 1];
 #pragma unroll
         for (int o = 0; o < S; ++o) {
+          const uint32_t base = mapa_shared(smem_u32(smem), 2 * o + rank);
 #pragma unroll
           for (int k = 0; k < U; ++k) {
             const int r = kq_min(r0 + k * STEP, 127);
-            x[o][k] = ld_dsmem_f4(base[o] + r * (NB * 4) + ((cc / 4) ^ (r & 7)) * 16);
+            x[o][k] = ld_dsmem_f4(base + r * (NB * 4) + ((cc / 4) ^ (r & 7)) * 16);
             if constexpr (GATED)
-              y[o][k] = ld_dsmem_f4(base[o] + r * (NB * 4) + ((cc / 4 + NB / 8) ^ (r & 7)) * 16);
+              y[o][k] = ld_dsmem_f4(base + r * (NB * 4) + ((cc / 4 + NB / 8) ^ (r & 7)) * 16);
           }
         }
 #pragma unroll
@@ -604,25 +639,13 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           const int r = r0 + k * STEP;
           const int64_t row = row0 + r;
           if (r >= warp * 16 + 16 || row >= p.M) continue;
-          float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+          float4 v = x[0][k], u = y[0][GATED ? k : 0];
 #pragma unroll
-          for (int o = 0; o < S; ++o) {
-            v[0] += x[o][k].x; v[1] += x[o][k].y; v[2] += x[o][k].z; v[3] += x[o][k].w;
-            if constexpr (GATED) {
-              u[0] += y[o][k].x; u[1] += y[o][k].y; u[2] += y[o][k].z; u[3] += y[o][k].w;
-            }
+          for (int o = 1; o < S; ++o) {
+            v = add4(v, x[o][k]);
+            if constexpr (GATED) u = add4(u, y[o][k]);
           }
-#pragma unroll
-          for (int t = 0; t < 4; ++t) v[t] += bias[t];
-          if (p.Z) store4(p.Z + row * p.ldz + col, v, n);
-          if (GATED && p.Z) store4(p.Z2 + row * p.ldz + col, u, n);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            v[t] = act_run(p.act, v[t]);
-            if (GATED) v[t] *= u[t];
-            else if (p.R) v[t] += t < n ? __bfloat162float(p.R[row * p.ldr + col + t]) : 0.f;
-          }
-          store4(p.Y + row * p.ldy + col, v, n);
+          finish4<GATED>(p, row, col, n, add4(v, bias), u);
         }
       }
     }
@@ -664,11 +687,11 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         const int64_t col = bj * NT + cc;
         if (col >= p.N || row0 >= p.M) break;
         if (p.Z) {
-#pragma unroll
+#pragma unroll 1
           for (int o = 0; o < (GATED ? 2 : 1); ++o) {
             uint8_t *slot = slots + (used++ & 1) * PSLOT;
             slot_free<false>(lane);
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               float v[32];
               tmem_ld32(tq + cc + NB / 2 * o + 32 * h, v);
@@ -687,7 +710,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           slot_free<false>(lane);
           if (!GATED && p.R) residual(slot, col);
         }
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           float v[32], u[GATED ? 32 : 1];
           tmem_ld32(tq + cc + 32 * h, v);
@@ -697,10 +720,22 @@ __global__ void __launch_bounds__(PTHREADS, 1)
             for (int k = 0; k < 32; ++k)
               v[k] += col + 32 * h + k < p.N ? __ldg(p.bias + col + 32 * h + k) : 0.f;
           }
+          if constexpr (ACT == KRONQ_ACT_GELU) {   // (long: one copy of its code)
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            v[k] = act_f<ACT>(v[k]);
-            if constexpr (GATED) v[k] *= u[k];
+            for (int k = 0; k < 32; k += 4) {
+              const float4 g = gelu4(make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
+              v[k] = g.x;
+              v[k + 1] = g.y;
+              v[k + 2] = g.z;
+              v[k + 3] = g.w;
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = act_f<ACT>(v[k]);
+          }
+          if constexpr (GATED) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= u[k];
           }
           if (!GATED && p.R) {
             if (h == 0) {
@@ -934,7 +969,7 @@ kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d,
   KQ_TRY(smem_attr(kern, C::SMEM));
   FewP p;
   p.d = d;
-  p.act = act;
+  p.d.act = act;
   p.tiles_t = static_cast<int>(ceil_div(d.M, NT));
   const int64_t tiles = p.tiles_t * ceil_div(d.N, DT);
   int64_t split = kq_min<int64_t>(kq_min<int64_t>(8, 148 * C::PER_SM / tiles),
@@ -1012,15 +1047,23 @@ kronq_status launch_pair(cudaStream_t st, const Operands &o, DenseP p, int act) 
   }
 }
 
-// Tokens per tile of the few-token kernel, 0 for the pair kernel.
-int few_width(int64_t tokens) {
-  return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 0;
+// Tokens per tile of the few-token kernel, 0 for the pair kernel. Above 64 tokens
+// the few-token kernel's partial sums cost as much as the weights they save,
+// unless K is long. Measured (us, few | pair), 128 tokens: 4096 -> 4096 13.0 | 14.6,
+// 11008 -> 4096 22.7 | 27.6, 1024 -> 8192 10.9 | 7.7, 1352 -> 2008 15.6 | 9.1, and
+// for the gated pair 4096 -> 2048 27.8 | 14.7, 1352 -> 1004 12.3 | 9.2; for the
+// pair at 64 tokens 4096 -> 2048 21.2 | 14.2 (its 16 tiles fill too few SMs),
+// 4096 -> 5504 22.1 | 27.1.
+int few_width(int64_t tokens, int64_t N, int64_t K, bool gated) {
+  if (tokens > 128 || (tokens > 64 && (gated || K < 4096))) return 0;
+  if (gated && tokens > 32 && N < 4096) return 0;
+  return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128;
 }
 
 // D = X W^T by the kernel that takes it: few tokens, or pairs
 template <bool GATED, bool W_MN>
 kronq_status tokens_product(cudaStream_t st, const Operands &o, const DenseP &p, int act) {
-  const int nt = few_width(p.M);
+  const int nt = few_width(p.M, p.N, p.K * p.nseg, GATED);
   if (nt == 0) return launch_pair<GATED, false, W_MN>(st, o, p, act);
   CUtensorMap tm[4];
   memset(tm, 0, sizeof(tm));
@@ -1032,8 +1075,9 @@ kronq_status tokens_product(cudaStream_t st, const Operands &o, const DenseP &p,
     case 16: return launch_few<GATED, W_MN, 16>(st, tm, p, act);
     case 32: return launch_few<GATED, W_MN, 32>(st, tm, p, act);
     case 64: return launch_few<GATED, W_MN, 64>(st, tm, p, act);
-    default: return launch_few<GATED, W_MN, 128>(st, tm, p, act);
   }
+  if constexpr (!GATED) return launch_few<GATED, W_MN, 128>(st, tm, p, act);
+  return KRONQ_ERR_UNSUPPORTED;   // (not reached)
 }
 
 // dX = G W (+ G2 W2) + R
