@@ -7,12 +7,9 @@
 // A row's maximum and sum of exponentials, the loss over the k kept entries,
 // the dense part of the gradient, and last the k places that the teacher
 // names, each written whole (a place named twice gets the same value twice).
-// distill_row_kernel keeps a narrow row in registers, distill_wide_kernel a
-// wider one in the shared memory of up to 8 CTAs; rows too wide for that (over
-// 281592 bf16 or 140796 fp32 logits) are read once per pass by distill_kernel. The exponent z/tau - lse is taken in base 2 as
-// z c - L with c = log2(e) / tau and L = lse log2(e); for fp32 logits both
-// constants are held in two parts, so that the exponent is off by half an ulp
-// of itself, not of its larger terms.
+// distill_wide_kernel keeps a row in the shared memory of up to 8 CTAs; rows too
+// wide for that (over 281592 bf16 or 140796 fp32 logits) are read once per pass
+// by distill_kernel. Exponentials are taken in base 2, with c = log2(e) / tau.
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -185,51 +182,38 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
   }
 }
 
-// ---------------------------------------------------------------- narrow rows
-// A CTA of 128 threads a row, eight an SM; the row stays in registers between
-// the sums and the gradient, up to VPT 16-byte vectors a thread, all loaded at
-// once, so the logits are read once and the gradient written once. Each thread
-// makes a pair (maximum m, sum s of exponentials relative to it) of its part
-// and one of its teacher entries; the pairs meet by warp and CTA in a fixed
-// order, scaled to the common maximum. q_v is then exp(z_v / tau - m) / s,
-// without a logarithm; the loss needs one, after the gradient is on its way.
-// Vectors are aligned addresses: the first and last of a row may hold places
-// outside it, which are not read and count as -inf.
-constexpr int VPT = 8;
-
+// ---------------------------------------------------------------- row on the chip
 template <class T>
 struct VecOf {
   static constexpr int E = 16 / sizeof(T);
 };
 
+// a vector's values in pairs
 template <class T>
-__device__ __forceinline__ void unpack(const uint4 &r, float *v) {
+__device__ __forceinline__ void unpack2(const uint4 &r, F2 *x) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
   if constexpr (sizeof(T) == 4) {
-    v[0] = __uint_as_float(r.x);
-    v[1] = __uint_as_float(r.y);
-    v[2] = __uint_as_float(r.z);
-    v[3] = __uint_as_float(r.w);
+    x[0] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    x[1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
   } else {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      v[2 * t] = __uint_as_float(w[t] << 16);
-      v[2 * t + 1] = __uint_as_float(w[t] & 0xffff0000u);
-    }
+    for (int t = 0; t < 4; ++t)
+      x[t] = f2(__uint_as_float(w[t] << 16), __uint_as_float(w[t] & 0xffff0000u));
   }
 }
-
-template <class T>
-__device__ __forceinline__ void store_vec(T *p, const float *v) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    uint4 o;
-    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&o);
+__device__ __forceinline__ void store_vec2(float *p, const F2 *x) {
+  const float2 a = f2_get(x[0]), b = f2_get(x[1]);
+  *reinterpret_cast<float4 *>(p) = make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store_vec2(__nv_bfloat16 *p, const F2 *x) {
+  uint4 o;
+  __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&o);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) h[t] = __floats2bfloat162_rn(v[2 * t], v[2 * t + 1]);
-    *reinterpret_cast<uint4 *>(p) = o;
+  for (int t = 0; t < 4; ++t) {
+    const float2 a = f2_get(x[t]);
+    h[t] = __floats2bfloat162_rn(a.x, a.y);
   }
+  *reinterpret_cast<uint4 *>(p) = o;
 }
 
 __device__ __forceinline__ float ex2(float a) {
@@ -238,16 +222,29 @@ __device__ __forceinline__ float ex2(float a) {
   return e;
 }
 
-// 2^((z - m) c): the difference first, so that its rounding is relative to it
+// 2^((z - m) c) of a pair. fp32: the difference first, so that its rounding is
+// relative to it. bf16: z c - m c in one step, relative to m c as rounded; the
+// rounding is a factor 1 + fix for all values with this m.
 template <class T>
-__device__ __forceinline__ float exp_rel(float z, float m, float c_hi, float c_lo) {
-  if constexpr (sizeof(T) == 4) {
-    const float d = max_nan(z - m, -1.0e30f);
-    return ex2(fmaf(d, c_hi, d * c_lo));
-  } else {
-    return ex2((z - m) * c_hi);
+struct Exponent {
+  F2 c, b;
+  float fix;
+  __device__ __forceinline__ Exponent(float m, float c1) {
+    c = f2(c1, c1);
+    if constexpr (sizeof(T) == 4) {
+      b = f2(-m, -m);
+      fix = 0.f;
+    } else {
+      const float mc = m * c1;
+      b = f2(-mc, -mc);
+      fix = -0.69314718f * fmaf(m, c1, -mc);
+    }
   }
-}
+  __device__ __forceinline__ F2 operator()(F2 z) const {
+    const float2 x = f2_get(sizeof(T) == 4 ? f2_mul(f2_add(z, b), c) : f2_fma(z, c, b));
+    return f2(ex2(x.x), ex2(x.y));
+  }
+};
 
 // (m, s) pairs: m may be -inf (then s is 0)
 __device__ __forceinline__ float rescale(float s, float from, float to, float c) {
@@ -268,215 +265,30 @@ __device__ __forceinline__ void warp_pair(float &m, float &s, float c) {
   m = wm;
 }
 
-template <class T, bool FWD, bool BWD, int THREADS>
-__global__ void __launch_bounds__(THREADS, 8)
-    distill_row_kernel(const DistillP a) {
-  constexpr int E = VecOf<T>::E, WARPS = THREADS / 32;
-  __shared__ __align__(16) float p_s[DI_MAXK], z_s[DI_MAXK];
-  __shared__ __align__(16) int32_t i_s[DI_MAXK];
-  __shared__ __align__(16) float4 wpair[WARPS];   // (m, s) of the row, (m, s) of the teacher
-  __shared__ double loss_s[WARPS];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t row = blockIdx.x;
-  const int vocab = static_cast<int>(a.vocab);
-  const T *z = static_cast<const T *>(a.Z) + row * a.ldz;
-  T *dz = static_cast<T *>(a.dZ) + row * a.lddz;
-  pdl_launch();
-  pdl_wait();
-  const float w = a.weight ? a.weight[row] : 1.f;
-  const bool live = w != 0.f;
-  const int head = static_cast<int>(reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
-  const int nvec = (vocab + head + E - 1) / E;
-  const float c2e = a.c_hi;                                 // log2(e) / tau
-
-  uint4 raw[VPT];
-  float tm = -INFINITY, ts = 0.f;     // the teacher's (m, s)
-  if (live) {
-    // ---- the teacher's entries, one a thread (k <= THREADS: no loop)
-    for (int j = tid; j < a.k; j += THREADS) {
-      i_s[j] = a.idx[row * a.ldt + j];
-      p_s[j] = a.t_bf16
-                   ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.T)[row * a.ldt + j])
-                   : static_cast<const float *>(a.T)[row * a.ldt + j];
-    }
-    // ---- the row's vectors, all in flight at once
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * THREADS + tid, e = v * E - head;
-      constexpr uint32_t NINF = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-      raw[i] = make_uint4(NINF, NINF, NINF, NINF);
-      if (v >= nvec) continue;
-      if (e >= 0 && e + E <= vocab) {
-        raw[i] = *reinterpret_cast<const uint4 *>(z + e);
-      } else {
-        uint32_t *r = reinterpret_cast<uint32_t *>(&raw[i]);
-#pragma unroll
-        for (int t = 0; t < E; ++t) {
-          if (e + t < 0 || e + t >= vocab) continue;
-          if constexpr (sizeof(T) == 4) {
-            r[t] = __float_as_uint(z[e + t]);
-          } else {
-            const uint32_t b = __bfloat16_as_ushort(z[e + t]);
-            r[t / 2] = t % 2 ? (r[t / 2] & 0xffffu) | b << 16 : (r[t / 2] & 0xffff0000u) | b;
-          }
-        }
-      }
-    }
-    for (int j = tid; j < a.k; j += THREADS) {
-      const int i = i_s[j];
-      const bool in = i >= 0 && i < vocab;
-      if (i >= vocab) report(a.info, KRONQ_ERR_INVALID_ARG);
-      const float t = in ? p_s[j] : -INFINITY;
-      z_s[j] = in ? to_f(z[i]) : 0.f;
-      i_s[j] = t != -INFINITY ? i : -1;
-      p_s[j] = t;
-      const float m2 = max_nan(tm, t);
-      ts = rescale(ts, tm, m2, c2e) + (t == -INFINITY ? 0.f : ex2((t - m2) * c2e));
-      tm = m2;
-    }
-  }
-  // ---- (m, s) of the row
-  float m = -INFINITY, s = 0.f;
-  if (live) {
-    if (FWD) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        float v[E];
-        unpack<T>(raw[i], v);
-#pragma unroll
-        for (int t = 0; t < E; ++t) m = max_nan(m, v[t]);
-      }
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      if (m != -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          float v[E];
-          unpack<T>(raw[i], v);
-#pragma unroll
-          for (int t = 0; t < E; ++t) acc[t % 4] += exp_rel<T>(v[t], m, a.c_hi, a.c_lo);
-        }
-      }
-      s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-      warp_pair(m, s, c2e);
-    }
-    warp_pair(tm, ts, c2e);
-    if (lane == 0) wpair[warp] = make_float4(m, s, tm, ts);
-  }
-  __syncthreads();
-  if (live) {
-    m = tm = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < WARPS; ++k) {
-      const float4 x = wpair[k];
-      m = max_nan(m, x.x);
-      tm = max_nan(tm, x.z);
-    }
-    s = ts = 0.f;
-#pragma unroll
-    for (int k = 0; k < WARPS; ++k) {
-      const float4 x = wpair[k];
-      if (FWD) s += rescale(x.y, x.x, m, c2e);
-      ts += rescale(x.w, x.z, tm, c2e);
-    }
-  }
-  const bool counts = live && tm != -INFINITY;   // some entry is kept
-  if (FWD) {
-    if (m < NO_LOGIT) m = NAN;   // no logit at all: q has no value
-  }
-  // ---- gradient
-  const float wt = w * a.tau;
-  float b_hi = 0.f, b_lo = 0.f, scale = wt;
-  if (BWD) {
-    if (FWD) {            // 2^(z c - m c) / s
-      b_hi = m * a.c_hi;
-      b_lo = fmaf(m, a.c_hi, -b_hi) + m * a.c_lo;
-      scale = __fdiv_rn(wt, s);
-    } else {              // 2^(z c - lse log2 e)
-      constexpr float L2E_HI = 1.44269502f, L2E_LO = 1.92596299e-8f;
-      const float lse = a.lse[row];
-      b_hi = lse * L2E_HI;
-      b_lo = fmaf(lse, L2E_HI, -b_hi) + lse * L2E_LO;
-    }
-    const bool vec = (reinterpret_cast<uintptr_t>(dz) & 15) == (reinterpret_cast<uintptr_t>(z) & 15);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * THREADS + tid, e = v * E - head;
-      if (v >= nvec) continue;
-      float g[E];
-      if (counts) {
-        unpack<T>(raw[i], g);
-#pragma unroll
-        for (int t = 0; t < E; ++t)
-          g[t] = scale * exp_term<T>(g[t], a.c_hi, a.c_lo, b_hi, b_lo);
-      } else {
-#pragma unroll
-        for (int t = 0; t < E; ++t) g[t] = 0.f;
-      }
-      if (vec && e >= 0 && e + E <= vocab) {
-        store_vec(dz + e, g);
-      } else {
-#pragma unroll
-        for (int t = 0; t < E; ++t)
-          if (e + t >= 0 && e + t < vocab) put(dz + e + t, g[t]);
-      }
-    }
-  }
-  // ---- loss; p_s becomes p
-  double loss = 0.0;
-  if (counts) {
-    for (int j = tid; j < a.k; j += THREADS) {
-      const float t = p_s[j];
-      const float p = i_s[j] >= 0 ? __fdiv_rn(ex2((t - tm) * c2e), ts) : 0.f;
-      p_s[j] = p;
-      if (FWD && p != 0.f)
-        loss += double(p) * ((double(t) - double(tm) - double(z_s[j]) + double(m)) * a.inv_tau +
-                             log(double(s) / double(ts)));
-    }
-    if (FWD && warp * 32 < a.k) {
-      loss = warp_sum_d(loss);
-      if (lane == 0) loss_s[warp] = loss;
-    }
-  }
-  __syncthreads();
-  if (FWD && tid == 0) {
-    float l = 0.f, lse = 0.f;
-    if (counts) {
-      for (int k = 1; k < WARPS && k * 32 < a.k; ++k) loss += loss_s[k];
-      l = float(double(a.tau) * double(a.tau) * loss);
-      lse = float(double(m) * a.inv_tau + log(double(s)));
-      if (!isfinite(l)) report(a.info, KRONQ_ERR_NONFINITE);
-    }
-    a.loss[row] = l;
-    if (a.lse) a.lse[row] = lse;
-  }
-  if (BWD && counts) {   // the places the teacher names
-    for (int j = tid; j < a.k; j += THREADS) {
-      const int i = i_s[j];
-      if (i < 0) continue;
-      float p = 0.f;
-      for (int l = 0; l < a.k; ++l) p += i_s[l] == i ? p_s[l] : 0.f;
-      put(dz + i, scale * exp_term<T>(z_s[j], a.c_hi, a.c_lo, b_hi, b_lo) - wt * p);
-    }
-  }
-}
-
-// ---------------------------------------------------------------- wide rows
-// For rows that take a CTA or several: a row lies over `parts` CTAs (with the
-// forward pass a cluster), each with its part in shared memory, where a bulk
-// copy brings it. The part is read there three times: maximum, sum of
+// A row lies in the shared memory of a CTA (or, over 70 KB, of a cluster of
+// them, the CTAs independent of one another in the backward pass alone), where
+// a bulk copy brings it. It is read there three times: maximum, sum of
 // exponentials, gradient. The CTAs are persistent and independent, several an
 // SM, so that the copies of some run under the arithmetic of others; while a
-// CTA's own copy is on its way it collects the teacher's entries of that row
-// and writes the rest of the row before (the places that the teacher names,
-// the loss).
+// CTA's own copy is on its way it writes the rest of the row before (the places
+// that the teacher names, the loss) and has the teacher's entries of the next.
+// Each thread makes a pair (maximum m, sum s of exponentials relative to it) of
+// its part of the row and one of its teacher entries; the pairs meet by warp,
+// CTA and cluster in a fixed order, scaled to the common maximum. q_v is then
+// exp(z_v / tau - m) / s, without a logarithm; the loss needs one a row.
 //   The copy takes whole 16-byte vectors inside the row; the threads that own
 // the row's first and last vector put those together when they are cut.
-//   Measured (4096 rows of 32000 bf16 logits, k = 64, gradient too): 107 us =
-// 4.9 TB/s with three CTAs an SM of 384 threads; two of 512 threads 120 us, six
-// of 192 threads on half rows (clusters of two) 121 us; a row kept in registers
-// and one CTA of 512 threads an SM 135 us (its phases do not overlap).
-constexpr int ST = 384;
-constexpr int WIDE_VEC = 4400;   // vectors of a part: 70 KB, three CTAs an SM
+//   Sizes: 384 threads and three CTAs an SM, or for rows of up to 22 KB 128
+// threads and up to nine, of up to 6 KB 64 threads and up to sixteen.
+// Measured (4096 rows of 32000 bf16 logits, k = 64, with the gradient): three
+// CTAs of 384 threads 107 us, two of 512 threads 120 us, six of 192 threads on
+// half rows (clusters of two) 121 us; the row in registers, one CTA of 512
+// threads an SM, 135 us (its phases do not overlap).
+constexpr int WIDE_VEC = 4400;   // vectors of a part at most: 70 KB
+template <int ST>
+constexpr int wide_per_sm() {
+  return ST == 384 ? 3 : ST == 128 ? 9 : 16;
+}
 
 // ln(x) for a normal x > 0, off by less than 4e-8: exponent times ln 2 in
 // fp64, plus the fp32 logarithm of a mantissa in [0.75, 1.5)
@@ -524,8 +336,8 @@ __device__ __forceinline__ uint4 cut_vec(const T *z, int e, int vocab) {
   return o;
 }
 
-template <class T, bool FWD, bool BWD>
-__global__ void __launch_bounds__(ST, 3)
+template <class T, bool FWD, bool BWD, int ST>
+__global__ void __launch_bounds__(ST, wide_per_sm<ST>())
     distill_wide_kernel(const DistillP a, int parts, int per, int kp, int n) {
   constexpr int E = VecOf<T>::E, WARPS = ST / 32;
   extern __shared__ __align__(128) uint8_t dsm[];
@@ -535,7 +347,7 @@ __global__ void __launch_bounds__(ST, 3)
   float *z_s = reinterpret_cast<float *>(i_s + 2 * kp);               // [2][kp]: z, then w tau q
   __shared__ __align__(16) float4 wpair[32];         // (m, s) of the row, of the teacher
   __shared__ __align__(16) float4 pair[2];           // the CTA's (m, s)
-  __shared__ double loss_s[WARPS];
+  __shared__ double2 loss_s[2][WARPS];
   __shared__ uint64_t bar;
   __shared__ int abort_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -586,12 +398,58 @@ __global__ void __launch_bounds__(ST, 3)
   };
   auto weight_of = [&](int64_t r) { return r >= n ? 0.f : a.weight ? a.weight[r] : 1.f; };
 
+  // the teacher's entry of this thread (entries past ST are read when needed)
+  auto entry = [&](int r, int j, int &i, float &t) {
+    const int64_t at = r * a.ldt + j;
+    i = a.idx[at];
+    t = a.t_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.T)[at])
+                 : static_cast<const float *>(a.T)[at];
+  };
+  // the student's logit there
+  auto logit_at = [&](int r, int i) { return i >= 0 && i < vocab ? row_ptr(r)[i] : T(0.f); };
+  // The loss and lse of a row from its (m, s), the teacher's sum and the
+  // warps' parts of sum p (T - max T - z) and sum p (one thread).
+  auto finish_row = [&](int r, bool counts, float m, float s, float ts, const double2 *parts_s) {
+    float l = 0.f, lse = 0.f;
+    if (counts) {
+      double x = 0.0, y = 0.0;
+      for (int q = 0; q < WARPS && q * 32 < k; ++q) {
+        x += parts_s[q].x;
+        y += parts_s[q].y;
+      }
+      const double ls = log_split(s);
+      l = float(double(a.tau) * double(a.tau) *
+                ((x + y * double(m)) * a.inv_tau + (ls - log_split(ts))));
+      lse = float(double(m) * a.inv_tau + ls);
+      if (!isfinite(l)) report(a.info, KRONQ_ERR_NONFINITE);
+    }
+    a.loss[r] = l;
+    if (a.lse) a.lse[r] = lse;
+  };
+  // (m, s) of the row from the cluster's pairs, a pair a lane
+  auto cluster_pair = [&](int par, float &m, float &s) {
+    const float4 x = lane < parts ? ld_dsmem_f4(mapa_shared(smem_u32(&pair[par]), lane))
+                                  : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    m = warp_max_nan(x.x);
+    s = warp_sum(rescale(x.y, x.x, m, c2e));
+  };
+
   int row = blockIdx.x / parts;
   float w = weight_of(row);
   if (w != 0.f) fetch(row);
+  int ni = -1;
+  float nt = 0.f;
+  T nz = T(0.f);
+  if (row < n && tid < k) {
+    entry(row, tid, ni, nt);
+    nz = logit_at(row, ni);
+  }
   uint32_t phase = 0;
   int par = 0;
   bool abort = false;       // a wait ran out: no more copies, the barriers go on
+  int last = -1;            // forward alone over a cluster: the row to be finished
+  float last_ts = 0.f;
+  bool last_counts = false;
   for (; row < n; par ^= 1) {
     const bool live = w != 0.f;
     const float w1 = weight_of(int64_t(row) + stride);
@@ -603,14 +461,16 @@ __global__ void __launch_bounds__(ST, 3)
     float tm = -INFINITY, ts = 0.f;
     if (live) {
       for (int j = tid; j < k; j += ST) {
-        const int64_t at = row * a.ldt + j;
-        int i = a.idx[at];
-        float t = a.t_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.T)[at])
-                           : static_cast<const float *>(a.T)[at];
+        int i = ni;
+        float t = nt, zj = to_f(nz);
+        if (j >= ST) {
+          entry(row, j, i, t);
+          zj = to_f(logit_at(row, i));
+        }
         if (i >= vocab) report(a.info, KRONQ_ERR_INVALID_ARG);
         if (i < 0 || i >= vocab) t = -INFINITY;
         if (t == -INFINITY) i = -1;
-        zr[j] = i >= 0 ? to_f(z[i]) : 0.f;
+        zr[j] = zj;
         tr[j] = t;
         ir[j] = i;
         const float m2 = max_nan(tm, t);
@@ -630,26 +490,28 @@ __global__ void __launch_bounds__(ST, 3)
 #pragma unroll 4
         for (int v = tid; v < cnt; v += ST) m = max_nan(m, max_vec<T>(buf[v]));
         m = m < NO_LOGIT ? NO_LOGIT : m;    // exponents of masked logits: -inf
-        const float mc = m * a.c_hi;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        const Exponent<T> ex(m, a.c_hi);
+        F2 acc0 = f2(0.f, 0.f), acc1 = acc0;
 #pragma unroll 4
         for (int v = tid; v < cnt; v += ST) {
-          float x[E];
-          unpack<T>(buf[v], x);
+          F2 x[E / 2];
+          unpack2<T>(buf[v], x);
 #pragma unroll
-          for (int t = 0; t < E; ++t)
-            acc[t % 4] += sizeof(T) == 4 ? exp_rel<T>(x[t], m, a.c_hi, a.c_lo)
-                                         : ex2(fmaf(x[t], a.c_hi, -mc));
+          for (int t = 0; t < E / 2; t += 2) {
+            acc0 = f2_add(acc0, ex(x[t]));
+            acc1 = f2_add(acc1, ex(x[t + 1]));
+          }
         }
-        s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-        // bf16: the exponentials are relative to mc as rounded
-        if (sizeof(T) == 2) s = fmaf(s, -0.69314718f * fmaf(m, a.c_hi, -mc), s);
+        const float2 sum = f2_get(f2_add(acc0, acc1));
+        s = sum.x + sum.y;
+        s = fmaf(s, ex.fix, s);
         warp_pair(m, s, c2e);
       }
     }
     if (lane == 0) wpair[warp] = make_float4(m, s, tm, ts);
     __syncthreads();
     if (!BWD && w1 != 0.f && !abort) fetch(row + stride);   // the buffer is free
+    if (stride < n - row && tid < k) entry(row + stride, tid, ni, nt);
     {
       const float4 x = wpair[lane];
       m = FWD ? warp_max_nan(x.x) : 0.f;
@@ -658,71 +520,112 @@ __global__ void __launch_bounds__(ST, 3)
       ts = warp_sum(rescale(x.w, x.z, tm, c2e));
     }
     const bool counts = live && tm != -INFINITY;   // some entry is kept
-    if (clus) {
+    if (clus && BWD) {
       if (tid == 0) pair[par] = make_float4(m, s, 0.f, 0.f);
       __syncwarp();
       cluster_sync_all();
-      const float4 x = lane < parts ? ld_dsmem_f4(mapa_shared(smem_u32(&pair[par]), lane))
-                                    : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      m = warp_max_nan(x.x);
-      s = warp_sum(rescale(x.y, x.x, m, c2e));
+      cluster_pair(par, m, s);
+    } else if (clus) {
+      // nothing here needs the whole row's (m, s): the barrier of a row is
+      // waited for a row later, and its loss finished then
+      if (last >= 0) {
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        if (rank == 0 && warp == WARPS - 1) {
+          float rm, rs;
+          cluster_pair(par ^ 1, rm, rs);
+          if (rm <= NO_LOGIT) rm = NAN;
+          if (lane == 31) finish_row(last, last_counts, rm, rs, last_ts, loss_s[par ^ 1]);
+        }
+      }
+      if (tid == 0) pair[par] = make_float4(m, s, 0.f, 0.f);
+      __syncwarp();
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      last = row;
+      last_ts = ts;
+      last_counts = counts;
     }
     if (FWD && m <= NO_LOGIT) m = NAN;   // no logit at all: q has no value
     // ---- the dense gradient
     const float wt = w * a.tau;
-    float b_hi = 0.f, b_lo = 0.f, scale = wt;
+    // The exponentials of the gradient: those of the sums, relative to the row's
+    // m, over s; in the backward pass alone relative to tau lse, of which the
+    // part that fp32 drops goes into the factor.
+    float ref = m, scale = 0.f, fix = 0.f;
     if (BWD) {
-      if (FWD) {            // 2^(z c - m c) / s
-        b_hi = m * a.c_hi;
-        b_lo = fmaf(m, a.c_hi, -b_hi) + m * a.c_lo;
-        scale = __fdiv_rn(wt, s);
-      } else {              // 2^(z c - lse log2 e)
-        constexpr float L2E_HI = 1.44269502f, L2E_LO = 1.92596299e-8f;
-        b_hi = lse_in * L2E_HI;
-        b_lo = fmaf(lse_in, L2E_HI, -b_hi) + lse_in * L2E_LO;
+      if (!FWD) {
+        const double r = double(lse_in) * double(a.tau);
+        ref = float(r);
+        fix = -0.69314718f * a.c_hi * float(r - double(ref));
       }
-      // bf16: the exponent's second part is the same for the whole row
-      if (sizeof(T) == 2) scale = fmaf(scale, -0.69314718f * b_lo, scale);
+      scale = FWD ? __fdiv_rn(wt, s) : wt;
+      const Exponent<T> ex(ref, a.c_hi);
+      fix += ex.fix;
+      scale = fmaf(scale, fix, scale);
       T *dz = static_cast<T *>(a.dZ) + int64_t(row) * a.lddz;
       const bool vec =
           (reinterpret_cast<uintptr_t>(dz) & 15) == (reinterpret_cast<uintptr_t>(z) & 15);
-#pragma unroll 2
-      for (int v = tid; v < cnt; v += ST) {
-        const int at = e0 + v * E;
-        float g[E];
-        unpack<T>(buf[v], g);
+      const F2 sc = f2(scale, scale);
+      // the vectors that the row fills and that are aligned in dZ too
+      const int lo = !vec ? cnt : e0 < 0 ? 1 : 0, hi = !vec ? cnt : e0 + cnt * E > vocab ? cnt - 1 : cnt;
+      if (counts) {
+#pragma unroll 4
+        for (int v = tid; v < hi; v += ST) {
+          if (v < lo) continue;
+          F2 x[E / 2];
+          unpack2<T>(buf[v], x);
 #pragma unroll
-        for (int t = 0; t < E; ++t)
-          g[t] = counts ? scale * exp_term<T>(g[t], a.c_hi, a.c_lo, b_hi, b_lo) : 0.f;
-        if (vec && at >= 0 && at + E <= vocab) {
-          store_vec(dz + at, g);
-        } else {
-          for (int t = 0; t < E; ++t)
-            if (at + t >= 0 && at + t < vocab) put(dz + at + t, g[t]);
+          for (int t = 0; t < E / 2; ++t) x[t] = f2_mul(ex(x[t]), sc);
+          store_vec2(dz + (e0 + v * E), x);
+        }
+      } else {
+        F2 x[E / 2];
+#pragma unroll
+        for (int t = 0; t < E / 2; ++t) x[t] = f2(0.f, 0.f);
+        for (int v = tid; v < hi; v += ST)
+          if (v >= lo) store_vec2(dz + (e0 + v * E), x);
+      }
+      // the others (at most the first and the last, or all of them) by element
+      for (int v = tid; v < cnt; v += ST) {
+        if (v >= lo && v < hi) continue;
+        F2 x[E / 2];
+        unpack2<T>(buf[v], x);
+        const int at = e0 + v * E;
+#pragma unroll
+        for (int t = 0; t < E / 2; ++t) {
+          const float2 g = f2_get(f2_mul(ex(x[t]), sc));
+          if (at + 2 * t >= 0 && at + 2 * t < vocab) put(dz + at + 2 * t, counts ? g.x : 0.f);
+          if (at + 2 * t + 1 >= 0 && at + 2 * t + 1 < vocab)
+            put(dz + at + 2 * t + 1, counts ? g.y : 0.f);
         }
       }
     }
     // ---- the teacher's p (kept as w tau p) and its part of the loss
-    if (counts) {
+    if (counts && warp * 32 < k) {
       const float rts = __fdiv_rn(1.f, ts);
-      double loss = 0.0;
+      double x = 0.0, y = 0.0;
       for (int j = tid; j < k; j += ST) {
         const float t = tr[j], zj = zr[j];
         const float p = ir[j] >= 0 ? ex2((t - tm) * c2e) * rts : 0.f;
-        if (FWD && rank == 0 && p != 0.f)
-          loss += double(p) * ((double(t) - double(tm) - double(zj) + double(m)) * a.inv_tau);
+        if (FWD && rank == 0 && p != 0.f) {
+          x += double(p) * (double(t) - double(tm) - double(zj));
+          y += double(p);
+        }
         if (BWD) {
           tr[j] = wt * p;
-          zr[j] = scale * exp_term<T>(zj, a.c_hi, a.c_lo, b_hi, b_lo);
+          const Exponent<T> ex(ref, a.c_hi);
+          zr[j] = scale * f2_get(ex(f2(zj, zj))).x;
         }
       }
-      if (FWD && rank == 0 && warp * 32 < k) {
-        loss = warp_sum_d(loss);
-        if (lane == 0) loss_s[warp] = loss;
+      if (FWD && rank == 0) {
+        __syncwarp();
+        x = warp_sum_d(x);
+        y = warp_sum_d(y);
+        if (lane == 0) loss_s[par][warp] = make_double2(x, y);
       }
     }
     __syncthreads();
     if (BWD && w1 != 0.f && !abort) fetch(row + stride);   // the buffer is free
+    if (stride < n - row && tid < k) nz = logit_at(row + stride, ni);
     // ---- the places the teacher names in this part, behind the dense stores:
     // w tau (q - the sum of the p of all entries that name the place)
     if (BWD && counts) {
@@ -745,22 +648,21 @@ __global__ void __launch_bounds__(ST, 3)
         put(dz + i, zr[j] - p);
       }
     }
-    if (FWD && rank == 0 && tid == ST - 1) {
-      float l = 0.f, lse = 0.f;
-      if (counts) {
-        double sum = 0.0;
-        for (int x = 0; x < WARPS && x * 32 < k; ++x) sum += loss_s[x];
-        const double ls = log_split(s);
-        l = float(double(a.tau) * double(a.tau) * (sum + (ls - log_split(ts))));
-        lse = float(double(m) * a.inv_tau + ls);
-        if (!isfinite(l)) report(a.info, KRONQ_ERR_NONFINITE);
-      }
-      a.loss[row] = l;
-      if (a.lse) a.lse[row] = lse;
-    }
+    if (FWD && (BWD || !clus) && rank == 0 && tid == ST - 1)
+      finish_row(row, counts, m, s, ts, loss_s[par]);
     w = w1;
     if (stride >= n - row) break;
     row += stride;
+  }
+  __syncwarp();
+  if (clus && !BWD && last >= 0) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank == 0 && warp == WARPS - 1) {
+      float rm, rs;
+      cluster_pair(par, rm, rs);
+      if (rm <= NO_LOGIT) rm = NAN;
+      if (lane == 31) finish_row(last, last_counts, rm, rs, last_ts, loss_s[par]);
+    }
   }
   if (abort) {   // a copy may still be in flight
     if (tid == 0) report(a.info, KRONQ_ERR_TIMEOUT);
@@ -810,28 +712,62 @@ kronq_status resident_rows(const void *kern, int threads, int smem, int parts, b
   return KRONQ_OK;
 }
 
-template <class T, bool FWD, bool BWD>
-kronq_status launch_wide(cudaStream_t st, const DistillP &p, int64_t n, int64_t nvec, int parts) {
-  auto *kern = distill_wide_kernel<T, FWD, BWD>;
-  const int per = static_cast<int>(ceil_div(nvec, parts)), kp = (p.k + 3) / 4 * 4;
-  const bool clus = FWD && parts > 1;
-  const int smem = (per * 16 + 24 * kp + 1023) / 1024 * 1024;
-  KQ_TRY(smem_attr(kern, smem));
-  int rows = 0;
-  KQ_TRY(resident_rows(reinterpret_cast<const void *>(kern), ST, smem, parts, clus, &rows));
-  rows = static_cast<int>(kq_min<int64_t>(n, rows));
-  return launch_kernel(st, kern, int64_t(rows) * parts, ST, smem, clus ? parts : 1, true, p, parts,
-                       per, kp, static_cast<int>(n));
+// A launch of distill_wide_kernel with rows over `parts` CTAs: its shared memory
+// and how many rows run at once.
+struct WidePlan {
+  int parts, per, kp, smem, rows;
+};
+template <class T, bool FWD, bool BWD, int ST>
+kronq_status plan_wide(const DistillP &p, int64_t nvec, int parts, WidePlan *w) {
+  auto *kern = distill_wide_kernel<T, FWD, BWD, ST>;
+  w->parts = parts;
+  w->per = static_cast<int>(ceil_div(nvec, parts));
+  w->kp = (p.k + 3) / 4 * 4;
+  w->smem = (w->per * 16 + 24 * w->kp + 1023) / 1024 * 1024;
+  KQ_TRY(smem_attr(kern, w->smem));
+  return resident_rows(reinterpret_cast<const void *>(kern), ST, w->smem, parts, FWD && parts > 1,
+                       &w->rows);
+}
+template <class T, bool FWD, bool BWD, int ST>
+kronq_status launch_wide(cudaStream_t st, const DistillP &p, int64_t n, const WidePlan &w) {
+  const int64_t rows = kq_min<int64_t>(n, w.rows);
+  return launch_kernel(st, distill_wide_kernel<T, FWD, BWD, ST>, rows * w.parts, ST, w.smem,
+                       FWD ? w.parts : 1, true, p, w.parts, w.per, w.kp, static_cast<int>(n));
 }
 
 template <class T, bool FWD, bool BWD>
 kronq_status launch_mode(cudaStream_t st, const DistillP &p, int64_t n) {
   // a row that starts off a 16-byte boundary touches one vector more
   const int64_t nvec = ceil_div(p.vocab, VecOf<T>::E) + 1;
-  if (nvec <= 128 * VPT)
-    return launch_kernel(st, distill_row_kernel<T, FWD, BWD, 128>, n, 128, 0, 1, true, p);
-  const int64_t parts = ceil_div(nvec, WIDE_VEC);
-  if (parts <= 8) return launch_wide<T, FWD, BWD>(st, p, n, nvec, static_cast<int>(parts));
+  WidePlan w;
+  if (nvec <= 384) {
+    KQ_TRY((plan_wide<T, FWD, BWD, 64>(p, nvec, 1, &w)));
+    return launch_wide<T, FWD, BWD, 64>(st, p, n, w);
+  }
+  if (nvec <= 1408) {
+    KQ_TRY((plan_wide<T, FWD, BWD, 128>(p, nvec, 1, &w)));
+    return launch_wide<T, FWD, BWD, 128>(st, p, n, w);
+  }
+  if (nvec <= 8 * WIDE_VEC) {
+    // Parts of a row: what makes the rounds of rows cheapest. A round costs its
+    // part plus about 1500 vectors' time for the barriers and the teacher's
+    // entries, 2500 more across a cluster. (Measured with the gradient: one row of
+    // 32000 bf16 logits 7.1 us in one part, 5.4 in eight; 300 rows of 50257 fp32
+    // logits 36.2 us in three parts, 33.2 in four; 64 rows of 8000 fp32 logits 4.9 us
+    // in one part, 6.0 in eight.)
+    WidePlan best = {};
+    int64_t best_cost = 0;
+    for (int parts = static_cast<int>(ceil_div(nvec, WIDE_VEC)); parts <= 8; ++parts) {
+      KQ_TRY((plan_wide<T, FWD, BWD, 384>(p, nvec, parts, &w)));
+      const int64_t cost =
+          ceil_div(n, w.rows) * (w.per + 1500 + (FWD && parts > 1 ? 2500 : 0));
+      if (best.parts == 0 || cost < best_cost) {
+        best = w;
+        best_cost = cost;
+      }
+    }
+    return launch_wide<T, FWD, BWD, 384>(st, p, n, best);
+  }
   return launch_kernel(st, distill_kernel<T, FWD, BWD>, n, DI_THREADS, 0, 1, false, p);
 }
 
