@@ -75,6 +75,17 @@ bool any_overlap(std::initializer_list<View> outs, std::initializer_list<View> i
   return false;
 }
 
+// Runs f; no C++ exception leaves the library (the launch helpers keep small
+// tables whose nodes are allocated on the host).
+template <class F>
+kronq_status guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    return KRONQ_ERR_CUDA;
+  }
+}
+
 bool act_ok(int a) { return a >= KRONQ_ACT_NONE && a <= KRONQ_ACT_GELU_TANH; }
 
 Mat mat(const View &v) { return Mat{const_cast<void *>(v.p), v.ld}; }
@@ -126,7 +137,7 @@ kronq_status run_distill(kronq_stream_t stream, const void *Z, kronq_dtype zdtyp
   a.dZ = dZ;
   a.lddz = lddz;
   a.info = info_dev;
-  return distill(as_stream(stream), a);
+  return guarded([&] { return distill(as_stream(stream), a); });
 }
 
 }  // namespace
@@ -473,8 +484,10 @@ kronq_status kronq_linear(kronq_stream_t stream, const void *X, int64_t n, int64
   if (n > kMaxRows || d_in > kMaxWidth || d_out > kMaxWidth) return KRONQ_ERR_UNSUPPORTED;
   if (n == 0) return KRONQ_OK;
   KQ_TRY(require_sm100());
-  return linear_fwd(as_stream(stream), n, d_in, d_out, mat(x), mat(w), bias, act, mat(z), mat(r),
-                    mat(y), info_dev);
+  return guarded([&] {
+    return linear_fwd(as_stream(stream), n, d_in, d_out, mat(x), mat(w), bias, act, mat(z), mat(r),
+                      mat(y), info_dev);
+  });
 }
 
 kronq_status kronq_linear_bwd(kronq_stream_t stream, const void *dY, int64_t lddy, const void *Z,
@@ -501,8 +514,10 @@ kronq_status kronq_linear_bwd(kronq_stream_t stream, const void *dY, int64_t ldd
     return KRONQ_ERR_INVALID_ARG;
   if (n > kMaxRows || d_in > kMaxWidth || d_out > kMaxWidth) return KRONQ_ERR_UNSUPPORTED;
   KQ_TRY(require_sm100());
-  return linear_bwd(as_stream(stream), n, d_in, d_out, mat(dy), mat(z), act, mat(x), mat(w),
-                    mat(dz), db, mat(dxr), mat(dx), mat(dw), info_dev);
+  return guarded([&] {
+    return linear_bwd(as_stream(stream), n, d_in, d_out, mat(dy), mat(z), act, mat(x), mat(w),
+                      mat(dz), db, mat(dxr), mat(dx), mat(dw), info_dev);
+  });
 }
 
 kronq_status kronq_gated(kronq_stream_t stream, const void *X, int64_t n, int64_t d, int64_t ldx,
@@ -520,8 +535,10 @@ kronq_status kronq_gated(kronq_stream_t stream, const void *X, int64_t n, int64_
   if (n > kMaxRows || d > kMaxWidth || f > kMaxWidth) return KRONQ_ERR_UNSUPPORTED;
   if (n == 0) return KRONQ_OK;
   KQ_TRY(require_sm100());
-  return gated_fwd(as_stream(stream), n, d, f, mat(x), mat(wg), mat(wu), act, mat(a), mat(u),
-                   mat(h), info_dev);
+  return guarded([&] {
+    return gated_fwd(as_stream(stream), n, d, f, mat(x), mat(wg), mat(wu), act, mat(a), mat(u),
+                     mat(h), info_dev);
+  });
 }
 
 kronq_status kronq_gated_bwd(kronq_stream_t stream, const void *dH, int64_t lddh, const void *A,
@@ -549,8 +566,10 @@ kronq_status kronq_gated_bwd(kronq_stream_t stream, const void *dH, int64_t lddh
     return KRONQ_ERR_INVALID_ARG;
   if (n > kMaxRows || d > kMaxWidth || f > kMaxWidth) return KRONQ_ERR_UNSUPPORTED;
   KQ_TRY(require_sm100());
-  return gated_bwd(as_stream(stream), n, d, f, mat(dh), mat(a), mat(u), act, mat(x), mat(wg),
-                   mat(wu), mat(gg), mat(gu), mat(dxr), mat(dx), mat(dwg), mat(dwu), info_dev);
+  return guarded([&] {
+    return gated_bwd(as_stream(stream), n, d, f, mat(dh), mat(a), mat(u), act, mat(x), mat(wg),
+                     mat(wu), mat(gg), mat(gu), mat(dxr), mat(dx), mat(dwg), mat(dwu), info_dev);
+  });
 }
 
 kronq_status kronq_distill_fwd(kronq_stream_t stream, const void *Z, kronq_dtype zdtype,

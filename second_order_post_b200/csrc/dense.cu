@@ -360,8 +360,11 @@ struct PairCtl {
 // NB: columns of the accumulator. A CTA's stage: 128 rows of A, NB / 2 of B.
 template <int NB>
 struct Pair {
-  static constexpr int STAGE = DPANEL + NB / 2 * DBK * 2;
-  static constexpr int STAGES = NB == 256 ? 5 : 6;
+  static constexpr int STAGE = DPANEL + (NB > 128 ? DPANEL : DPANEL / 2);
+  static constexpr int STAGES = NB > 128 ? 5 : 6;
+  // bytes of B that land in a CTA's stage: MN-major panels come in 64-wide boxes
+  static constexpr int BYTES_K = NB / 2 * 128, BYTES_MN = (NB / 2 + 63) / 64 * 64 * 128;
+  static constexpr int TMEM = NB > 128 ? 512 : 256;
   static constexpr int SMEM = STAGES * STAGE + 16 * PSLOT + 1024 + int(sizeof(PairCtl<STAGES>)) + 64;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(STAGES * STAGE >= 128 * NB * 4, "the partial sums fit in the ring");
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
     prefetch_tmap(&tmB);
   }
   __syncthreads();
-  if (warp == 9) tmem_alloc_pair(&ctl->tmem_base, 2 * NB);
+  if (warp == 9) tmem_alloc_pair(&ctl->tmem_base, C::TMEM);
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           const bool second = kb + it >= p.nk1;
           const int32_t k0 = (second ? kb + it - p.nk1 : kb + it) * DBK;
           const uint32_t bar = full0 + s * 8;
-          if (rank == 0) mbar_expect_tx(&ctl->full[s], 2 * PSTAGE);
+          if (rank == 0) mbar_expect_tx(&ctl->full[s], 2 * (DPANEL + (B_MN ? C::BYTES_MN : C::BYTES_K)));
           load_panel_pair<128>(st, second ? &tmA2 : &tmA, bar, A_MN, m0, k0);
           load_panel_pair<NB / 2>(st + DPANEL, (GATED ? rank != 0 : second) ? &tmB2 : &tmB, bar,
                                   B_MN, n0, k0);
@@ -669,11 +672,10 @@ __global__ void __launch_bounds__(PTHREADS, 1)
                      bytes > 0 ? p.R + row * p.ldr + c : p.R, bytes);
         }
       };
-      // columns of this half: NT / 2, or, where that is less than a slot, all of
-      // them for the first half
-      constexpr int MINE = NT >= 128 ? NT / 128 : 1;
-      const bool busy = NT >= 128 || half == 0;
-      const int first = NT >= 128 ? half * (NT / 2) : 0;
+      // slots of 64 columns of this half: the first half takes the odd one
+      constexpr int SLOTS = NT / 64, FIRST = (SLOTS + 1) / 2;
+      const int mine = half == 0 ? FIRST : SLOTS - FIRST, first = half * FIRST * 64;
+      const bool busy = mine > 0;
       const bool early = !GATED && busy && p.R && !p.Z;   // the first output takes R
       if (early) {
         slot_free<false>(lane);
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       const bool ok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      for (int c = 0; c < MINE && busy; ++c) {
+      for (int c = 0; c < mine; ++c) {
         const int cc = first + 64 * c;
         const int64_t col = bj * NT + cc;
         if (col >= p.N || row0 >= p.M) break;
@@ -787,7 +789,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
   cluster_sync_all();
   if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc_pair(tbase, 2 * NB);
+    tmem_dealloc_pair(tbase, C::TMEM);
   }
 }
 
@@ -980,21 +982,29 @@ kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d,
 }
 
 // How a product runs on pairs: columns of the accumulator and pairs a tile.
-//   A round of 74 pairs takes about nk * 520 + 6000 cycles at 256 columns and
-// nk * 320 + 5000 at 128 (nk slabs of k). Where a single round leaves pairs idle, k is
-// split over two or four of them if the clusters that takes all fit on the chip
-// (33 of four CTAs of this size, 15 of eight) and at least 8 slabs remain each.
+//   A round of 74 pairs takes about nk * 520 + 6000 cycles at 256 columns,
+// nk * 440 + 5500 at 192 (480 with B MN-major, whose panels of 96 rows load as 128)
+// and nk * 320 + 5000 at 128 (nk slabs of k): tiles are as wide as the number of
+// rounds lets them. Measured (us, 256 | 192 columns): 2000 tokens 3000 -> 5000 66.9 |
+// 63.8, its input gradient 80.2 | 73.3, 304 tokens 2504 -> 10000 40.0 | 33.1, but 4096
+// tokens 4096 -> 4096 111.7 | 115.7.
+//   Where a single round leaves pairs idle, k is split over two or four of them if
+// the clusters that takes all fit on the chip (33 of four CTAs of this size, 15 of
+// eight) and at least 8 slabs remain each: 256 tokens 4096 -> 4096 take 15.1 us in
+// two parts, 19.5 in one.
 struct PairPlan {
   int nb, split;
 };
-PairPlan pair_plan(int64_t rows, int64_t cols, int nk, bool gated) {
+PairPlan pair_plan(int64_t rows, int64_t cols, int nk, bool gated, bool b_mn) {
   const int64_t tm = ceil_div(rows, 256);
   const int64_t wide = tm * ceil_div(cols, gated ? 128 : 256);
   const int64_t narrow = tm * ceil_div(cols, gated ? 64 : 128);
   if (narrow <= 15 && nk >= 32) return {128, 4};
   if (narrow <= 33 && nk >= 16) return {128, 2};
   const int64_t c256 = ceil_div(wide, 74) * (int64_t(nk) * 520 + 6000);
+  const int64_t c192 = ceil_div(tm * ceil_div(cols, 192), 74) * (int64_t(nk) * (b_mn ? 480 : 440) + 5500);
   const int64_t c128 = ceil_div(narrow, 74) * (int64_t(nk) * 320 + 5000);
+  if (!gated && c192 < c256 && c192 < c128) return {192, 1};   // (no gated tiles of 96)
   return {c128 < c256 ? 128 : 256, 1};
 }
 
@@ -1005,7 +1015,7 @@ struct Operands {
 // D (M x N) = A B^T on pairs, A = (o.X, o.X2), B = (o.W, o.W2)
 template <bool GATED, bool A_MN, bool B_MN>
 kronq_status launch_pair(cudaStream_t st, const Operands &o, DenseP p, int act) {
-  const PairPlan plan = pair_plan(p.M, p.N, p.nk1 * p.nseg, GATED);
+  const PairPlan plan = pair_plan(p.M, p.N, p.nk1 * p.nseg, GATED, B_MN);
   CUtensorMap tm[4];
   memset(tm, 0, sizeof(tm));
   KQ_TRY(operand_map(&tm[0], o.X.p, o.X.ld, A_MN, p.M, p.K, 128));
@@ -1035,15 +1045,20 @@ kronq_status launch_pair(cudaStream_t st, const Operands &o, DenseP p, int act) 
   using I2 = std::integral_constant<int, 2>;
   using I4 = std::integral_constant<int, 4>;
   using N128 = std::integral_constant<int, 128>;
+  using N192 = std::integral_constant<int, GATED ? 256 : 192>;
   using N256 = std::integral_constant<int, 256>;
   if (plan.split == 4) return go(I0(), I4(), N128());   // (split tiles: p.act)
   if (plan.split == 2) return go(I0(), I2(), N128());
   if constexpr (!A_MN && !B_MN) {
     return with_act(act, [&](auto a) {
-      return plan.nb == 128 ? go(a, I1(), N128()) : go(a, I1(), N256());
+      return plan.nb == 128   ? go(a, I1(), N128())
+             : plan.nb == 192 ? go(a, I1(), N192())
+                              : go(a, I1(), N256());
     });
   } else {
-    return plan.nb == 128 ? go(I0(), I1(), N128()) : go(I0(), I1(), N256());
+    return plan.nb == 128   ? go(I0(), I1(), N128())
+           : plan.nb == 192 ? go(I0(), I1(), N192())
+                            : go(I0(), I1(), N256());
   }
 }
 

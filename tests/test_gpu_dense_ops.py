@@ -30,6 +30,11 @@ def _info():
     return torch.zeros(1, dtype=torch.int32, device="cuda")
 
 
+# many column tiles (tiles of 192 columns, several rounds of a persistent CTA), and
+# few of them with a long k (k split over the CTAs of a cluster)
+WIDE = [(304, 136, 10003), (513, 10001, 70), (2000, 260, 5000), (130, 4100, 200), (300, 6000, 520)]
+
+
 @pytest.mark.parametrize("size", SIZES)
 @pytest.mark.parametrize("act", ACTS)
 def test_linear(cuda_device, size, act):
@@ -60,6 +65,15 @@ def test_linear(cuda_device, size, act):
     if keep:
         close(Z, z, e + HALF_BF16 * (z.abs() + e) + 1e-30)
         assert untouched(zbuf, d_out)
+
+
+@pytest.mark.parametrize("size", WIDE)
+def test_linear_many_and_few_tiles(cuda_device, size):
+    test_linear(cuda_device, size, "silu")
+    test_linear(cuda_device, size, "none")
+    test_linear_bwd(cuda_device, size, "none")
+    test_gated(cuda_device, size, "gelu")
+    test_gated_bwd(cuda_device, size, "silu")
 
 
 def test_linear_in_place_residual(cuda_device):
@@ -368,6 +382,81 @@ def test_captured_and_replayed(cuda_device):
     assert info.item() == 0
     for a, b, c in zip(eager, one, two):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+def test_two_streams_at_once(cuda_device):
+    """Calls that overlap on the GPU (large and small products, distillation,
+    a covariance) share nothing: each gives what it gives alone."""
+    K = kq()
+    info = _info()
+    X, W = matrix(700, 1024, 1), matrix(1536, 1024, 2, 0.03)
+    x, Wg, Wu = matrix(3, 2048, 3), matrix(1024, 2048, 4, 0.02), matrix(1024, 2048, 5, 0.02)
+    Z = matrix(200, 9000, 6, 2.0)
+    T = torch.randn(200, 8, generator=torch.Generator().manual_seed(7)).cuda()
+    idx = torch.randint(0, 9000, (200, 8), generator=torch.Generator().manual_seed(8)).int().cuda()
+
+    def calls():
+        Y, H = out_like(700, 1536)[0], out_like(3, 1024)[0]
+        dZ, loss = torch.empty_like(Z), torch.empty(200, device="cuda")
+        cov = torch.empty(1024, 1024, device="cuda")
+        cinfo = torch.zeros(1, dtype=torch.int32, device="cuda")
+        return (Y, H, dZ, loss, cov), [
+            lambda s: K.kronq_linear(X, W, Y, info, act=K.KRONQ_ACT_SILU, stream=s),
+            lambda s: K.kronq_gated(x, Wg, Wu, H, info, stream=s),
+            lambda s: K.kronq_distill_step(Z, T, idx, loss, None, dZ, info, stream=s),
+            lambda s: K.kronq_accum_cov(X, cov, 1.0, 0.0, cinfo, stream=s)]
+
+    want, alone = calls()
+    for c in alone:
+        c(None)
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for turn in range(4):
+        got, both = calls()
+        torch.cuda.synchronize()
+        for rep in range(3):
+            for k, c in enumerate(both):
+                c(streams[(k + turn) % 4])
+        torch.cuda.synchronize()
+        assert info.item() == 0
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_first_call_of_a_process_captured(cuda_device):
+    """The first use of the operators in a process may be under capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from second_order_post_b200 import kronq as K
+g = torch.Generator(device="cuda"); g.manual_seed(0)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+X, W, Y, H = r(300, 256), r(512, 256), r(300, 512), r(300, 256)
+Z, T = r(40, 40000), torch.randn(40, 4, device="cuda")
+idx = torch.zeros(40, 4, dtype=torch.int32, device="cuda")
+loss, dZ = torch.empty(40, device="cuda"), torch.empty_like(Z)
+info = torch.zeros(1, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+def go():
+    K.kronq_linear(X, W, Y, info)
+    K.kronq_gated(X[:4], W[:256], W[256:], H[:4], info)
+    K.kronq_distill_step(Z, T, idx, loss, None, dZ, info)
+with torch.cuda.graph(graph):
+    go()
+graph.replay()
+torch.cuda.synchronize()
+a = [t.clone() for t in (Y, H, loss, dZ)]
+go()
+torch.cuda.synchronize()
+assert info.item() == 0 and all(torch.equal(x, y) for x, y in zip(a, (Y, H, loss, dZ)))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and "same" in out.stdout, out.stderr[-2000:]
 
 
 def test_same_bits_twice(cuda_device):
