@@ -961,9 +961,19 @@ kronq_status operand_map(CUtensorMap *m, const void *p, int64_t ld, bool mn, int
             : make_tmap_2d(m, p, true, K, rows, ld, DBK, box_rows);
 }
 
-// How a product is launched: the few-token kernel splits k over `split` CTAs
-// of a cluster, as many as fit on the chip at once with at least two slabs
-// each.
+// How many clusters of n CTAs are on the chip at once: they do not reach over the
+// groups of SMs it is made of, some of which have fewer SMs.
+int few_clusters(int per_sm, int n) {
+  static constexpr int one[9] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+  static constexpr int two[9] = {0, 296, 148, 93, 71, 56, 45, 34, 33};
+  return per_sm == 2 ? two[n] : one[n];
+}
+
+// The few-token kernel splits k over the CTAs of a cluster, as many as leave two
+// slabs each and are all on the chip at once: one token 4096 -> 5120 (40 tiles) takes
+// 9.7 us in six parts and 13.9 in seven, of which 34 clusters are on the chip. Five
+// to seven parts pay for one tile of 16 tokens only: 64 tokens 4096 -> 6016 take 17.8
+// in five, 14.7 in four (the sums of the parts are shared out evenly over four).
 template <bool GATED, bool W_MN, int NT>
 kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d, int act) {
   using C = Few<GATED, NT>;
@@ -974,9 +984,12 @@ kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d,
   p.d.act = act;
   p.tiles_t = static_cast<int>(ceil_div(d.M, NT));
   const int64_t tiles = p.tiles_t * ceil_div(d.N, DT);
-  int64_t split = kq_min<int64_t>(kq_min<int64_t>(8, 148 * C::PER_SM / tiles),
-                                  d.nk1 * d.nseg / 2);
-  p.split = static_cast<int>(kq_max<int64_t>(split, 1));
+  p.split = static_cast<int>(
+      kq_min<int64_t>(kq_min<int64_t>(8, 148 * C::PER_SM / tiles), d.nk1 * d.nseg / 2));
+  while (p.split > 1 && (tiles > few_clusters(C::PER_SM, p.split) ||
+                         (NT > 16 && p.split > 4 && p.split < 8)))
+    --p.split;
+  p.split = kq_max(p.split, 1);
   return launch_kernel(st, kern, tiles * p.split, FTHREADS, C::SMEM, p.split, true, tm[0], tm[1],
                        tm[2], tm[3], p);
 }
@@ -990,8 +1003,9 @@ kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d,
 // tokens 4096 -> 4096 111.7 | 115.7.
 //   Where a single round leaves pairs idle, k is split over two or four of them if
 // the clusters that takes all fit on the chip (33 of four CTAs of this size, 15 of
-// eight) and at least 8 slabs remain each: 256 tokens 4096 -> 4096 take 15.1 us in
-// two parts, 19.5 in one.
+// eight) and enough slabs remain each: 256 tokens 4096 -> 4096 take 15.2 us in two
+// parts and 19.3 in one, 200 tokens 8192 -> 1024 11.7 in four and 26.0 in one, but
+// 250 tokens 1024 -> 1024 7.0 in two and 6.5 in one.
 struct PairPlan {
   int nb, split;
 };
@@ -1000,7 +1014,7 @@ PairPlan pair_plan(int64_t rows, int64_t cols, int nk, bool gated, bool b_mn) {
   const int64_t wide = tm * ceil_div(cols, gated ? 128 : 256);
   const int64_t narrow = tm * ceil_div(cols, gated ? 64 : 128);
   if (narrow <= 15 && nk >= 32) return {128, 4};
-  if (narrow <= 33 && nk >= 16) return {128, 2};
+  if (narrow <= 33 && nk >= 20) return {128, 2};
   const int64_t c256 = ceil_div(wide, 74) * (int64_t(nk) * 520 + 6000);
   const int64_t c192 = ceil_div(tm * ceil_div(cols, 192), 74) * (int64_t(nk) * (b_mn ? 480 : 440) + 5500);
   const int64_t c128 = ceil_div(narrow, 74) * (int64_t(nk) * 320 + 5000);
