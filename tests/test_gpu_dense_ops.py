@@ -508,3 +508,24 @@ def test_binding_refuses(cuda_device):
         K.kronq_gated(X, W, W, Y, info, A=out_like(n, d_out)[0])      # A without U
     torch.cuda.synchronize()
     assert info.item() == 0
+
+
+@pytest.mark.parametrize("act", [a for a in ACTS if a != "none"])
+def test_activation_at_every_bf16_value(act):
+    """Value and derivative at every bf16 number of magnitude 2^-20 to 32 (z = X
+    with W the identity, dY = 1). The tolerance leaves 2^-20 of the value (2^-20 of 1
+    for the derivative, which crosses zero) for the evaluation next to the rounding."""
+    k = kq()
+    bits = torch.arange((127 - 20) << 7, (127 + 5) << 7, dtype=torch.int32)
+    pos = bits.to(torch.int16).view(torch.bfloat16)
+    X = torch.cat([pos, -pos]).view(-1, 64).cuda()
+    W = torch.eye(64, dtype=torch.bfloat16, device="cuda")
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    Y, dZ, ones = torch.empty_like(X), torch.empty_like(X), torch.ones_like(X)
+    k.kronq_linear(X, W, Y, info, act=k.KRONQ_ACTS[act])
+    k.kronq_linear_bwd(ones, X, None, info, act=k.KRONQ_ACTS[act], Z=X, dZ=dZ)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    y, dy = act64(X.double(), act)
+    close(Y, y, (EVAL + HALF_BF16) * y.abs() + 1e-30)
+    close(dZ, dy, EVAL * LIP + HALF_BF16 * dy.abs())
