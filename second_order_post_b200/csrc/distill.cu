@@ -7,9 +7,10 @@
 // A row's maximum and sum of exponentials, the loss over the k kept entries,
 // the dense part of the gradient, and last the k places that the teacher
 // names, each written whole (a place named twice gets the same value twice).
-// distill_wide_kernel keeps a row in the shared memory of up to 8 CTAs; rows too
-// wide for that (over 281592 bf16 or 140796 fp32 logits) are read once per pass
-// by distill_kernel. Exponentials are taken in base 2, with c = log2(e) / tau.
+// With the gradient, distill_wide_kernel keeps a row in the shared memory of up to
+// 8 CTAs, and rows too wide for that (over 281592 bf16 or 140796 fp32 logits) are
+// read once per pass by distill_kernel. The loss alone needs a row once: streamed
+// by distill_fwd_kernel. Exponentials are taken in base 2, with c = log2(e) / tau.
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -78,7 +79,7 @@ __device__ __forceinline__ V block_reduce(V v, V *red, V zero, F f) {
   return v;
 }
 
-template <class T, bool FWD, bool BWD>
+template <class T, bool FWD>
 __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
   __shared__ float p_s[DI_MAXK], z_s[DI_MAXK];
   __shared__ int32_t i_s[DI_MAXK];
@@ -115,8 +116,7 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
       a.loss[row] = 0.f;
       if (a.lse) a.lse[row] = 0.f;
     }
-    if (BWD)
-      for (int64_t v = tid; v < a.vocab; v += DI_THREADS) put(dz + v, 0.f);
+    for (int64_t v = tid; v < a.vocab; v += DI_THREADS) put(dz + v, 0.f);
     return;
   }
   tmax = block_reduce(tmax, red, -INFINITY, [](float x, float y) { return fmaxf(x, y); });
@@ -164,21 +164,19 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
   }
 
   // ---- gradient
-  if (BWD) {
-    const double L = lse * 1.4426950408889634074;
-    const float b_hi = float(L), b_lo = float(L - double(b_hi));
-    const float wt = w * a.tau;
-    __syncthreads();
-    for (int64_t v = tid; v < a.vocab; v += DI_THREADS)
-      put(dz + v, wt * exp_term<T>(to_f(z[v]), a.c_hi, a.c_lo, b_hi, b_lo));
-    __syncthreads();
-    for (int j = tid; j < a.k; j += DI_THREADS) {
-      const int32_t i = i_s[j];
-      if (i < 0) continue;
-      float p = 0.f;
-      for (int l = 0; l < a.k; ++l) p += i_s[l] == i ? p_s[l] : 0.f;
-      put(dz + i, wt * (exp_term<T>(z_s[j], a.c_hi, a.c_lo, b_hi, b_lo) - p));
-    }
+  const double L = lse * 1.4426950408889634074;
+  const float b_hi = float(L), b_lo = float(L - double(b_hi));
+  const float wt = w * a.tau;
+  __syncthreads();
+  for (int64_t v = tid; v < a.vocab; v += DI_THREADS)
+    put(dz + v, wt * exp_term<T>(to_f(z[v]), a.c_hi, a.c_lo, b_hi, b_lo));
+  __syncthreads();
+  for (int j = tid; j < a.k; j += DI_THREADS) {
+    const int32_t i = i_s[j];
+    if (i < 0) continue;
+    float p = 0.f;
+    for (int l = 0; l < a.k; ++l) p += i_s[l] == i ? p_s[l] : 0.f;
+    put(dz + i, wt * (exp_term<T>(z_s[j], a.c_hi, a.c_lo, b_hi, b_lo) - p));
   }
 }
 
@@ -265,8 +263,8 @@ __device__ __forceinline__ void warp_pair(float &m, float &s, float c) {
   m = wm;
 }
 
-// A row lies in the shared memory of a CTA (or, over 70 KB, of a cluster of
-// them, the CTAs independent of one another in the backward pass alone), where
+// With the gradient. A row lies in the shared memory of a CTA (or, over 70 KB, of a
+// cluster of them, independent CTAs in the backward pass alone), where
 // a bulk copy brings it. It is read there three times: maximum, sum of
 // exponentials, gradient. The CTAs are persistent and independent, several an
 // SM, so that the copies of some run under the arithmetic of others; while a
@@ -319,7 +317,7 @@ __device__ __forceinline__ uint4 neg_inf_vec() {
 
 // The vector at element e of a row of `vocab`, places outside it -inf.
 template <class T>
-__device__ __forceinline__ uint4 cut_vec(const T *z, int e, int vocab) {
+__device__ __forceinline__ uint4 cut_vec(const T *z, int64_t e, int64_t vocab) {
   constexpr int E = VecOf<T>::E;
   uint4 o = neg_inf_vec<T>();
   uint32_t *r = reinterpret_cast<uint32_t *>(&o);
@@ -336,7 +334,28 @@ __device__ __forceinline__ uint4 cut_vec(const T *z, int e, int vocab) {
   return o;
 }
 
-template <class T, bool FWD, bool BWD, int ST>
+// The loss and lse of a row from its (m, s), the teacher's sum and the warps' parts
+// of sum p (T - max T - z) and sum p (one thread).
+__device__ __forceinline__ void finish_loss(const DistillP &a, int64_t r, bool counts, float m,
+                                            float s, float ts, const double2 *parts_s, int np) {
+  float l = 0.f, lse = 0.f;
+  if (counts) {
+    double x = 0.0, y = 0.0;
+    for (int q = 0; q < np; ++q) {
+      x += parts_s[q].x;
+      y += parts_s[q].y;
+    }
+    const double ls = log_split(s);
+    l = float(double(a.tau) * double(a.tau) *
+              ((x + y * double(m)) * a.inv_tau + (ls - log_split(ts))));
+    lse = float(double(m) * a.inv_tau + ls);
+    if (!isfinite(l)) report(a.info, KRONQ_ERR_NONFINITE);
+  }
+  a.loss[r] = l;
+  if (a.lse) a.lse[r] = lse;
+}
+
+template <class T, bool FWD, int ST>
 __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
     distill_wide_kernel(const DistillP a, int parts, int per, int kp, int n) {
   constexpr int E = VecOf<T>::E, WARPS = ST / 32;
@@ -355,6 +374,7 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
   const int rank = blockIdx.x % parts, vocab = static_cast<int>(a.vocab), k = a.k;
   const int stride = gridDim.x / parts;
   const float c2e = a.c_hi;
+  const int lw = kq_min(WARPS, (k + 31) / 32);   // warps with teacher entries
   if (tid == 0) {
     mbar_init(&bar, 1);
     abort_s = 0;
@@ -407,33 +427,6 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
   };
   // the student's logit there
   auto logit_at = [&](int r, int i) { return i >= 0 && i < vocab ? row_ptr(r)[i] : T(0.f); };
-  // The loss and lse of a row from its (m, s), the teacher's sum and the
-  // warps' parts of sum p (T - max T - z) and sum p (one thread).
-  auto finish_row = [&](int r, bool counts, float m, float s, float ts, const double2 *parts_s) {
-    float l = 0.f, lse = 0.f;
-    if (counts) {
-      double x = 0.0, y = 0.0;
-      for (int q = 0; q < WARPS && q * 32 < k; ++q) {
-        x += parts_s[q].x;
-        y += parts_s[q].y;
-      }
-      const double ls = log_split(s);
-      l = float(double(a.tau) * double(a.tau) *
-                ((x + y * double(m)) * a.inv_tau + (ls - log_split(ts))));
-      lse = float(double(m) * a.inv_tau + ls);
-      if (!isfinite(l)) report(a.info, KRONQ_ERR_NONFINITE);
-    }
-    a.loss[r] = l;
-    if (a.lse) a.lse[r] = lse;
-  };
-  // (m, s) of the row from the cluster's pairs, a pair a lane
-  auto cluster_pair = [&](int par, float &m, float &s) {
-    const float4 x = lane < parts ? ld_dsmem_f4(mapa_shared(smem_u32(&pair[par]), lane))
-                                  : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    m = warp_max_nan(x.x);
-    s = warp_sum(rescale(x.y, x.x, m, c2e));
-  };
-
   int row = blockIdx.x / parts;
   float w = weight_of(row);
   if (w != 0.f) fetch(row);
@@ -447,9 +440,6 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
   uint32_t phase = 0;
   int par = 0;
   bool abort = false;       // a wait ran out: no more copies, the barriers go on
-  int last = -1;            // forward alone over a cluster: the row to be finished
-  float last_ts = 0.f;
-  bool last_counts = false;
   for (; row < n; par ^= 1) {
     const bool live = w != 0.f;
     const float w1 = weight_of(int64_t(row) + stride);
@@ -510,7 +500,6 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
     }
     if (lane == 0) wpair[warp] = make_float4(m, s, tm, ts);
     __syncthreads();
-    if (!BWD && w1 != 0.f && !abort) fetch(row + stride);   // the buffer is free
     if (stride < n - row && tid < k) entry(row + stride, tid, ni, nt);
     {
       const float4 x = wpair[lane];
@@ -520,29 +509,14 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
       ts = warp_sum(rescale(x.w, x.z, tm, c2e));
     }
     const bool counts = live && tm != -INFINITY;   // some entry is kept
-    if (clus && BWD) {
+    if (clus) {
       if (tid == 0) pair[par] = make_float4(m, s, 0.f, 0.f);
       __syncwarp();
       cluster_sync_all();
-      cluster_pair(par, m, s);
-    } else if (clus) {
-      // nothing here needs the whole row's (m, s): the barrier of a row is
-      // waited for a row later, and its loss finished then
-      if (last >= 0) {
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        if (rank == 0 && warp == WARPS - 1) {
-          float rm, rs;
-          cluster_pair(par ^ 1, rm, rs);
-          if (rm <= NO_LOGIT) rm = NAN;
-          if (lane == 31) finish_row(last, last_counts, rm, rs, last_ts, loss_s[par ^ 1]);
-        }
-      }
-      if (tid == 0) pair[par] = make_float4(m, s, 0.f, 0.f);
-      __syncwarp();
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-      last = row;
-      last_ts = ts;
-      last_counts = counts;
+      const float4 x = lane < parts ? ld_dsmem_f4(mapa_shared(smem_u32(&pair[par]), lane))
+                                    : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      m = warp_max_nan(x.x);
+      s = warp_sum(rescale(x.y, x.x, m, c2e));
     }
     if (FWD && m <= NO_LOGIT) m = NAN;   // no logit at all: q has no value
     // ---- the dense gradient
@@ -551,52 +525,50 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
     // m, over s; in the backward pass alone relative to tau lse, of which the
     // part that fp32 drops goes into the factor.
     float ref = m, scale = 0.f, fix = 0.f;
-    if (BWD) {
-      if (!FWD) {
-        const double r = double(lse_in) * double(a.tau);
-        ref = float(r);
-        fix = -0.69314718f * a.c_hi * float(r - double(ref));
-      }
-      scale = FWD ? __fdiv_rn(wt, s) : wt;
-      const Exponent<T> ex(ref, a.c_hi);
-      fix += ex.fix;
-      scale = fmaf(scale, fix, scale);
-      T *dz = static_cast<T *>(a.dZ) + int64_t(row) * a.lddz;
-      const bool vec =
-          (reinterpret_cast<uintptr_t>(dz) & 15) == (reinterpret_cast<uintptr_t>(z) & 15);
-      const F2 sc = f2(scale, scale);
-      // the vectors that the row fills and that are aligned in dZ too
-      const int lo = !vec ? cnt : e0 < 0 ? 1 : 0, hi = !vec ? cnt : e0 + cnt * E > vocab ? cnt - 1 : cnt;
-      if (counts) {
+    if (!FWD) {
+      const double r = double(lse_in) * double(a.tau);
+      ref = float(r);
+      fix = -0.69314718f * a.c_hi * float(r - double(ref));
+    }
+    scale = FWD ? __fdiv_rn(wt, s) : wt;
+    const Exponent<T> ex(ref, a.c_hi);
+    fix += ex.fix;
+    scale = fmaf(scale, fix, scale);
+    T *dz = static_cast<T *>(a.dZ) + int64_t(row) * a.lddz;
+    const bool vec =
+        (reinterpret_cast<uintptr_t>(dz) & 15) == (reinterpret_cast<uintptr_t>(z) & 15);
+    const F2 sc = f2(scale, scale);
+    // the vectors that the row fills and that are aligned in dZ too
+    const int lo = !vec ? cnt : e0 < 0 ? 1 : 0, hi = !vec ? cnt : e0 + cnt * E > vocab ? cnt - 1 : cnt;
+    if (counts) {
 #pragma unroll 4
-        for (int v = tid; v < hi; v += ST) {
-          if (v < lo) continue;
-          F2 x[E / 2];
-          unpack2<T>(buf[v], x);
-#pragma unroll
-          for (int t = 0; t < E / 2; ++t) x[t] = f2_mul(ex(x[t]), sc);
-          store_vec2(dz + (e0 + v * E), x);
-        }
-      } else {
-        F2 x[E / 2];
-#pragma unroll
-        for (int t = 0; t < E / 2; ++t) x[t] = f2(0.f, 0.f);
-        for (int v = tid; v < hi; v += ST)
-          if (v >= lo) store_vec2(dz + (e0 + v * E), x);
-      }
-      // the others (at most the first and the last, or all of them) by element
-      for (int v = tid; v < cnt; v += ST) {
-        if (v >= lo && v < hi) continue;
+      for (int v = tid; v < hi; v += ST) {
+        if (v < lo) continue;
         F2 x[E / 2];
         unpack2<T>(buf[v], x);
-        const int at = e0 + v * E;
 #pragma unroll
-        for (int t = 0; t < E / 2; ++t) {
-          const float2 g = f2_get(f2_mul(ex(x[t]), sc));
-          if (at + 2 * t >= 0 && at + 2 * t < vocab) put(dz + at + 2 * t, counts ? g.x : 0.f);
-          if (at + 2 * t + 1 >= 0 && at + 2 * t + 1 < vocab)
-            put(dz + at + 2 * t + 1, counts ? g.y : 0.f);
-        }
+        for (int t = 0; t < E / 2; ++t) x[t] = f2_mul(ex(x[t]), sc);
+        store_vec2(dz + (e0 + v * E), x);
+      }
+    } else {
+      F2 x[E / 2];
+#pragma unroll
+      for (int t = 0; t < E / 2; ++t) x[t] = f2(0.f, 0.f);
+      for (int v = tid; v < hi; v += ST)
+        if (v >= lo) store_vec2(dz + (e0 + v * E), x);
+    }
+    // the others (at most the first and the last, or all of them) by element
+    for (int v = tid; v < cnt; v += ST) {
+      if (v >= lo && v < hi) continue;
+      F2 x[E / 2];
+      unpack2<T>(buf[v], x);
+      const int at = e0 + v * E;
+#pragma unroll
+      for (int t = 0; t < E / 2; ++t) {
+        const float2 g = f2_get(f2_mul(ex(x[t]), sc));
+        if (at + 2 * t >= 0 && at + 2 * t < vocab) put(dz + at + 2 * t, counts ? g.x : 0.f);
+        if (at + 2 * t + 1 >= 0 && at + 2 * t + 1 < vocab)
+          put(dz + at + 2 * t + 1, counts ? g.y : 0.f);
       }
     }
     // ---- the teacher's p (kept as w tau p) and its part of the loss
@@ -610,11 +582,8 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
           x += double(p) * (double(t) - double(tm) - double(zj));
           y += double(p);
         }
-        if (BWD) {
-          tr[j] = wt * p;
-          const Exponent<T> ex(ref, a.c_hi);
-          zr[j] = scale * f2_get(ex(f2(zj, zj))).x;
-        }
+        tr[j] = wt * p;
+        zr[j] = scale * f2_get(ex(f2(zj, zj))).x;
       }
       if (FWD && rank == 0) {
         __syncwarp();
@@ -624,12 +593,11 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
       }
     }
     __syncthreads();
-    if (BWD && w1 != 0.f && !abort) fetch(row + stride);   // the buffer is free
+    if (w1 != 0.f && !abort) fetch(row + stride);   // the buffer is free
     if (stride < n - row && tid < k) nz = logit_at(row + stride, ni);
     // ---- the places the teacher names in this part, behind the dense stores:
     // w tau (q - the sum of the p of all entries that name the place)
-    if (BWD && counts) {
-      T *dz = static_cast<T *>(a.dZ) + int64_t(row) * a.lddz;
+    if (counts) {
       const int4 *pl = reinterpret_cast<const int4 *>(ir);
       const float4 *pp = reinterpret_cast<const float4 *>(tr);
       for (int j = tid; j < k; j += ST) {
@@ -648,21 +616,11 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
         put(dz + i, zr[j] - p);
       }
     }
-    if (FWD && (BWD || !clus) && rank == 0 && tid == ST - 1)
-      finish_row(row, counts, m, s, ts, loss_s[par]);
+    if (FWD && rank == 0 && tid == ST - 1)
+      finish_loss(a, row, counts, m, s, ts, loss_s[par], lw);
     w = w1;
     if (stride >= n - row) break;
     row += stride;
-  }
-  __syncwarp();
-  if (clus && !BWD && last >= 0) {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (rank == 0 && warp == WARPS - 1) {
-      float rm, rs;
-      cluster_pair(par, rm, rs);
-      if (rm <= NO_LOGIT) rm = NAN;
-      if (lane == 31) finish_row(last, last_counts, rm, rs, last_ts, loss_s[par]);
-    }
   }
   if (abort) {   // a copy may still be in flight
     if (tid == 0) report(a.info, KRONQ_ERR_TIMEOUT);
@@ -673,6 +631,197 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
   __syncwarp();
   // no CTA leaves while another may still read its pair
   if (clus) cluster_sync_all();
+}
+
+// ---------------------------------------------------------------- forward alone
+// Nothing needs a row twice, so it is streamed through registers: a CTA per row,
+// or a cluster of them when rows are few. Each thread takes FWD_U vectors at a
+// time, raises its maximum to theirs (its sum is rescaled only when that rises)
+// and adds their exponentials; the pairs meet as above. The places that the
+// teacher names are read by the first CTA under the first vectors' way.
+constexpr int FWD_U = 4;
+template <class T, int ST>
+__global__ void __launch_bounds__(ST, 1024 / ST)
+    distill_fwd_kernel(const DistillP a, int parts) {
+  constexpr int E = VecOf<T>::E, WARPS = ST / 32;
+  __shared__ float t_s[DI_MAXK], z_s[DI_MAXK];
+  __shared__ __align__(16) float4 wpair[WARPS];
+  __shared__ __align__(16) float4 pair;
+  __shared__ double2 loss_s[WARPS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % parts, k = a.k;
+  const int64_t row = blockIdx.x / parts;
+  const float c2e = a.c_hi;
+  pdl_launch();
+  pdl_wait();
+  const float w = a.weight ? a.weight[row] : 1.f;
+  if (w == 0.f) {   // (the whole cluster)
+    if (rank == 0 && tid == 0) {
+      a.loss[row] = 0.f;
+      if (a.lse) a.lse[row] = 0.f;
+    }
+    return;
+  }
+  const T *z = static_cast<const T *>(a.Z) + row * a.ldz;
+  const int64_t head = static_cast<int64_t>(reinterpret_cast<uintptr_t>(z) % 16 / sizeof(T));
+  const int64_t nvec = (a.vocab + head + E - 1) / E, per = (nvec + parts - 1) / parts;
+  const int64_t v0 = rank * per, v1 = kq_min<int64_t>(v0 + per, nvec);
+  // whole vectors
+  const int64_t w0 = v0 == 0 && head ? 1 : v0;
+  const int64_t w1 = v1 == nvec && nvec * E - head > a.vocab ? v1 - 1 : v1;
+  const uint4 *zv = reinterpret_cast<const uint4 *>(z - head);
+  float m = -INFINITY, s = 0.f;
+  auto add = [&](const uint4 *x) {
+    float top = max_vec<T>(x[0]);
+#pragma unroll
+    for (int u = 1; u < FWD_U; ++u) top = max_nan(top, max_vec<T>(x[u]));
+    top = max_nan(m, top < NO_LOGIT ? NO_LOGIT : top);   // exponents of masked logits: -inf
+    if (!(top == m)) {
+      s = rescale(s, m, top, c2e);
+      m = top;
+    }
+    const Exponent<T> ex(m, c2e);
+    F2 acc0 = f2(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+    for (int u = 0; u < FWD_U; ++u) {
+      F2 y[E / 2];
+      unpack2<T>(x[u], y);
+#pragma unroll
+      for (int t = 0; t < E / 2; t += 2) {
+        acc0 = f2_add(acc0, ex(y[t]));
+        acc1 = f2_add(acc1, ex(y[t + 1]));
+      }
+    }
+    const float2 sum = f2_get(f2_add(acc0, acc1));
+    s += fmaf(sum.x + sum.y, ex.fix, sum.x + sum.y);
+  };
+  auto load = [&](int64_t v, uint4 *x) {
+#pragma unroll
+    for (int u = 0; u < FWD_U; ++u) {
+      const int64_t at = v + u * ST;
+      x[u] = at < w1 ? __ldg(zv + at) : neg_inf_vec<T>();
+    }
+  };
+  uint4 x[FWD_U];
+  int64_t v = w0 + tid;
+  load(v, x);
+  // ---- the teacher's entries
+  float tm = -INFINITY, ts = 0.f;
+  if (rank == 0) {
+    for (int j = tid; j < k; j += ST) {
+      const int64_t at = row * a.ldt + j;
+      const int i = a.idx[at];
+      float t = a.t_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.T)[at])
+                         : static_cast<const float *>(a.T)[at];
+      if (i >= a.vocab) report(a.info, KRONQ_ERR_INVALID_ARG);
+      const bool in = i >= 0 && i < a.vocab;
+      if (!in) t = -INFINITY;
+      t_s[j] = t;
+      z_s[j] = in ? to_f(z[i]) : 0.f;
+      const float m2 = max_nan(tm, t);
+      ts = rescale(ts, tm, m2, c2e) + (t == -INFINITY ? 0.f : ex2((t - m2) * c2e));
+      tm = m2;
+    }
+    if (warp * 32 < k) warp_pair(tm, ts, c2e);
+  }
+  // ---- (m, s) of this part
+  while (v < w1) {   // (the vectors of the next step are on their way)
+    uint4 y[FWD_U];
+    v += FWD_U * ST;
+    load(v, y);
+    add(x);
+    if (v >= w1) break;
+    v += FWD_U * ST;
+    load(v, x);
+    add(y);
+  }
+  if (tid == 0 && v0 < w0) {
+#pragma unroll
+    for (int u = 0; u < FWD_U; ++u) x[u] = neg_inf_vec<T>();
+    x[0] = cut_vec(z, -head, a.vocab);
+    add(x);
+  }
+  if (tid == ST - 1 && w1 < v1 && w1 >= w0) {
+#pragma unroll
+    for (int u = 0; u < FWD_U; ++u) x[u] = neg_inf_vec<T>();
+    x[0] = cut_vec(z, w1 * E - head, a.vocab);
+    add(x);
+  }
+  warp_pair(m, s, c2e);
+  if (lane == 0) wpair[warp] = make_float4(m, s, tm, ts);
+  __syncthreads();
+  {
+    const float4 q = lane < WARPS ? wpair[lane] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    m = warp_max_nan(q.x);
+    tm = warp_max_nan(q.z);
+    s = warp_sum(rescale(q.y, q.x, m, c2e));
+    ts = warp_sum(rescale(q.w, q.z, tm, c2e));
+  }
+  if (parts > 1) {
+    if (tid == 0) pair = make_float4(m, s, 0.f, 0.f);
+    __syncwarp();
+    cluster_sync_all();
+    if (rank == 0) {
+      const float4 q = lane < parts ? ld_dsmem_f4(mapa_shared(smem_u32(&pair), lane))
+                                    : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      m = warp_max_nan(q.x);
+      s = warp_sum(rescale(q.y, q.x, m, c2e));
+    }
+  }
+  // ---- the loss
+  if (rank == 0) {
+    const bool counts = tm != -INFINITY;   // some entry is kept
+    const float rts = __fdiv_rn(1.f, ts);
+    double x0 = 0.0, y0 = 0.0;
+    if (counts) {
+      for (int j = tid; j < k; j += ST) {
+        const float t = t_s[j];
+        const float p = t == -INFINITY ? 0.f : ex2((t - tm) * c2e) * rts;
+        if (p != 0.f) {
+          x0 += double(p) * (double(t) - double(tm) - double(z_s[j]));
+          y0 += double(p);
+        }
+      }
+    }
+    x0 = warp_sum_d(x0);
+    y0 = warp_sum_d(y0);
+    if (lane == 0) loss_s[warp] = make_double2(x0, y0);
+    __syncthreads();
+    if (tid == 0) {
+      if (m <= NO_LOGIT) m = NAN;   // no logit at all: q has no value
+      finish_loss(a, row, counts, m, s, ts, loss_s, kq_min(WARPS, (k + 31) / 32));
+    }
+  }
+  __syncwarp();
+  // no CTA leaves while another may still read its pair
+  if (parts > 1) cluster_sync_all();
+}
+
+// Threads of a row: as many as fill the chip at 1024 an SM, with four vectors each
+// at least and 40 at most; above 512 they are CTAs of a cluster. Measured with 64 |
+// 128 | 256 | 512 threads: 4096 rows of 32000 bf16 logits 52.3 | 50.0 | 55.5 | 75.8 us,
+// 768 of 128256 60.6 | 51.5 | 40.0 | 40.6, 2048 of 6000 8.6 | 9.9 | 13.8 | 26.2,
+// 257 rows of 50257 fp32 logits 31.2 | 19.5 | 14.7 | 12.0; 8 rows of 128256 bf16
+// logits 8.1 with 512 and 4.6 with 4096; 100 of 128256 fp32 logits 14.7 with 1024
+// and 20.3 with 2048, which take a wave and a third.
+template <class T>
+kronq_status launch_fwd(cudaStream_t st, const DistillP &p, int64_t n) {
+  const int64_t nvec = ceil_div(p.vocab, VecOf<T>::E) + 1;
+  int threads = 64;   // the power of two next to a limit by the row's length
+  while (threads < 4096 && (threads * 10 < nvec / 40 * 7 ||
+                            (threads * 10 < nvec / 4 * 7 && threads * 2 * n <= 148 * 1024)))
+    threads *= 2;
+  const int parts = kq_max(threads / 512, 1);
+  auto go = [&](auto st_c) {
+    constexpr int ST = decltype(st_c)::value;
+    return launch_kernel(st, distill_fwd_kernel<T, ST>, n * parts, ST, 0, parts, true, p, parts);
+  };
+  switch (threads) {
+    case 64: return go(std::integral_constant<int, 64>());
+    case 128: return go(std::integral_constant<int, 128>());
+    case 256: return go(std::integral_constant<int, 256>());
+    default: return go(std::integral_constant<int, 512>());
+  }
 }
 
 // How many rows (clusters of `parts` CTAs) are on the chip at once; asked once
@@ -717,9 +866,9 @@ kronq_status resident_rows(const void *kern, int threads, int smem, int parts, b
 struct WidePlan {
   int parts, per, kp, smem, rows;
 };
-template <class T, bool FWD, bool BWD, int ST>
+template <class T, bool FWD, int ST>
 kronq_status plan_wide(const DistillP &p, int64_t nvec, int parts, WidePlan *w) {
-  auto *kern = distill_wide_kernel<T, FWD, BWD, ST>;
+  auto *kern = distill_wide_kernel<T, FWD, ST>;
   w->parts = parts;
   w->per = static_cast<int>(ceil_div(nvec, parts));
   w->kp = (p.k + 3) / 4 * 4;
@@ -728,25 +877,25 @@ kronq_status plan_wide(const DistillP &p, int64_t nvec, int parts, WidePlan *w) 
   return resident_rows(reinterpret_cast<const void *>(kern), ST, w->smem, parts, FWD && parts > 1,
                        &w->rows);
 }
-template <class T, bool FWD, bool BWD, int ST>
+template <class T, bool FWD, int ST>
 kronq_status launch_wide(cudaStream_t st, const DistillP &p, int64_t n, const WidePlan &w) {
   const int64_t rows = kq_min<int64_t>(n, w.rows);
-  return launch_kernel(st, distill_wide_kernel<T, FWD, BWD, ST>, rows * w.parts, ST, w.smem,
+  return launch_kernel(st, distill_wide_kernel<T, FWD, ST>, rows * w.parts, ST, w.smem,
                        FWD ? w.parts : 1, true, p, w.parts, w.per, w.kp, static_cast<int>(n));
 }
 
-template <class T, bool FWD, bool BWD>
-kronq_status launch_mode(cudaStream_t st, const DistillP &p, int64_t n) {
+template <class T, bool FWD>
+kronq_status launch_grad(cudaStream_t st, const DistillP &p, int64_t n) {
   // a row that starts off a 16-byte boundary touches one vector more
   const int64_t nvec = ceil_div(p.vocab, VecOf<T>::E) + 1;
   WidePlan w;
   if (nvec <= 384) {
-    KQ_TRY((plan_wide<T, FWD, BWD, 64>(p, nvec, 1, &w)));
-    return launch_wide<T, FWD, BWD, 64>(st, p, n, w);
+    KQ_TRY((plan_wide<T, FWD, 64>(p, nvec, 1, &w)));
+    return launch_wide<T, FWD, 64>(st, p, n, w);
   }
   if (nvec <= 1408) {
-    KQ_TRY((plan_wide<T, FWD, BWD, 128>(p, nvec, 1, &w)));
-    return launch_wide<T, FWD, BWD, 128>(st, p, n, w);
+    KQ_TRY((plan_wide<T, FWD, 128>(p, nvec, 1, &w)));
+    return launch_wide<T, FWD, 128>(st, p, n, w);
   }
   if (nvec <= 8 * WIDE_VEC) {
     // Parts of a row: what makes the rounds of rows cheapest. A round costs its
@@ -758,7 +907,7 @@ kronq_status launch_mode(cudaStream_t st, const DistillP &p, int64_t n) {
     WidePlan best = {};
     int64_t best_cost = 0;
     for (int parts = static_cast<int>(ceil_div(nvec, WIDE_VEC)); parts <= 8; ++parts) {
-      KQ_TRY((plan_wide<T, FWD, BWD, 384>(p, nvec, parts, &w)));
+      KQ_TRY((plan_wide<T, FWD, 384>(p, nvec, parts, &w)));
       const int64_t cost =
           ceil_div(n, w.rows) * (w.per + 1500 + (FWD && parts > 1 ? 2500 : 0));
       if (best.parts == 0 || cost < best_cost) {
@@ -766,16 +915,16 @@ kronq_status launch_mode(cudaStream_t st, const DistillP &p, int64_t n) {
         best_cost = cost;
       }
     }
-    return launch_wide<T, FWD, BWD, 384>(st, p, n, best);
+    return launch_wide<T, FWD, 384>(st, p, n, best);
   }
-  return launch_kernel(st, distill_kernel<T, FWD, BWD>, n, DI_THREADS, 0, 1, false, p);
+  return launch_kernel(st, distill_kernel<T, FWD>, n, DI_THREADS, 0, 1, false, p);
 }
 
 template <class T>
 kronq_status launch(cudaStream_t st, const DistillP &p, int64_t n, bool fwd, bool bwd) {
-  return fwd && bwd ? launch_mode<T, true, true>(st, p, n)
-         : fwd      ? launch_mode<T, true, false>(st, p, n)
-                    : launch_mode<T, false, true>(st, p, n);
+  return !bwd  ? launch_fwd<T>(st, p, n)
+         : fwd ? launch_grad<T, true>(st, p, n)
+               : launch_grad<T, false>(st, p, n);
 }
 
 }  // namespace

@@ -112,6 +112,27 @@ def test_distill(cuda_device, size, dtype, fused):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [(2500, 37, 5), (1300, 1501, 40), (700, 4500, 9),
+                                  (200, 20003, 600)])
+def test_forward_of_many_rows(cuda_device, size, dtype):
+    """More rows than the chip takes at once, from few to many threads a row, some
+    rows without weight; the logits start off 16-byte boundaries."""
+    n, vocab, k = size
+    Z, T, idx, w = _case(n, vocab, k, dtype, seed=vocab, pad=3)
+    w[::7] = 0.0
+    K = kq()
+    loss, lse = torch.full((n,), 9.0, device="cuda"), torch.full((n,), 9.0, device="cuda")
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    K.kronq_distill_fwd(Z, T, idx, loss, lse, info, tau=1.5, weight=w)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    want = _want(Z, T, idx, 1.5, w)
+    b_loss, b_lse, _ = _bounds(Z, T, idx, 1.5, w, want)
+    close(loss, want[0], b_loss)
+    close(lse, want[1], b_lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("vocab", [321, 40000])
 def test_rows_that_do_not_count(cuda_device, dtype, vocab):
     """Weight 0 (with NaN logits), nothing kept, teacher logits of -inf, and
