@@ -133,6 +133,31 @@ def test_forward_of_many_rows(cuda_device, size, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [(9, 50, 40), (3, 3000, 700), (2, 40000, 1024)])
+def test_places_named_often(cuda_device, size, dtype):
+    """Places that one to hundreds of entries name, next to places named once: each
+    is written once, with the sum of its entries, and the same way every time."""
+    n, vocab, k = size
+    Z, T, idx, w = _case(n, vocab, min(k, vocab), dtype, seed=k)
+    g = torch.Generator().manual_seed(vocab)
+    hot = torch.randint(0, vocab, (n, k), generator=g)
+    hot = torch.where(torch.rand(n, k, generator=g) < 0.3, hot % 5 + vocab // 2, hot)
+    hot[:, k // 3:k // 3 + 6] = torch.arange(6) // 2 * (vocab // 4)   # pairs
+    hot[0, :k // 2] = vocab - 1
+    idx = hot.int().cuda()
+    T = (Z.double().gather(1, idx.long()) + torch.randn(n, k, generator=g).cuda()).float()
+    for fused in (True, False):
+        loss, lse, dZ, info = _run(Z, T, idx, 2.0, w, fused)
+        assert info == 0
+        want = _want(Z, T, idx, 2.0, w)
+        b_loss, b_lse, b_dz = _bounds(Z, T, idx, 2.0, w, want)
+        close(loss, want[0], b_loss)
+        close(lse, want[1], b_lse)
+        close(dZ, want[2], b_dz)
+        assert torch.equal(dZ, _run(Z, T, idx, 2.0, w, fused)[2])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("vocab", [321, 40000])
 def test_rows_that_do_not_count(cuda_device, dtype, vocab):
     """Weight 0 (with NaN logits), nothing kept, teacher logits of -inf, and
