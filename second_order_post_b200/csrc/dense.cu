@@ -417,8 +417,8 @@ __device__ __forceinline__ void slot_out(const CUtensorMap *map, __nv_bfloat16 *
   fence_proxy_async_smem();
   __syncwarp();
   const int64_t n8 = N & ~int64_t(7);
-  if (lane == 0 && col < n8) {
-    tma_store_2d(map, slot, static_cast<int32_t>(col), static_cast<int32_t>(row));
+  if (lane == 0) {   // (a group for every slot, empty or not: slot_free counts them)
+    if (col < n8) tma_store_2d(map, slot, static_cast<int32_t>(col), static_cast<int32_t>(row));
     bulk_commit();
   }
   if (n8 < N && n8 - col < 64 && n8 >= col && row + lane < M) {

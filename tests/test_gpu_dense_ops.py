@@ -76,6 +76,15 @@ def test_linear_many_and_few_tiles(cuda_device, size):
     test_gated_bwd(cuda_device, size, "silu")
 
 
+@pytest.mark.parametrize("size", [(4500, 72, 1027), (5000, 40, 1089)])
+def test_last_columns_alone_in_their_slot(cuda_device, size):
+    """Several tiles a CTA, the last block of 64 columns fewer than eight wide: the
+    staging slot that holds them is written out by lanes, its turn counts all the same."""
+    test_linear(cuda_device, size, "none")
+    test_linear(cuda_device, size, "silu")
+    test_gated(cuda_device, size, "relu")
+
+
 def test_linear_in_place_residual(cuda_device):
     K = kq()
     n, d_in, d_out = 300, 256, 392
