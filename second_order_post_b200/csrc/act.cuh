@@ -66,8 +66,6 @@ static __device__ __noinline__ float4 act4(int act, float4 z) {
     default: return z;
   }
 }
-static __device__ __noinline__ float4 gelu4(float4 z) { return act4_f<KRONQ_ACT_GELU>(z); }
-
 // value and derivative
 template <int ACT>
 __device__ __forceinline__ void act_df(float z, float &h, float &dh) {

@@ -687,6 +687,16 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         slot_free<false>(lane);
         residual(slots + (used & 1) * PSLOT, bj * NT + first);
       }
+      // the bias of this half's columns, 32 a register, before it is needed
+      constexpr int BREGS = GATED ? 1 : 2 * FIRST;
+      float bias[BREGS];
+      if constexpr (!GATED) {
+#pragma unroll
+        for (int k = 0; k < BREGS; ++k) {
+          const int64_t col = bj * NT + first + 32 * k + lane;
+          bias[k] = p.bias && k < 2 * mine && col < p.N ? __ldg(p.bias + col) : 0.f;
+        }
+      }
       const bool ok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
@@ -694,28 +704,30 @@ __global__ void __launch_bounds__(PTHREADS, 1)
         const int cc = first + 64 * c;
         const int64_t col = bj * NT + cc;
         if (col >= p.N || row0 >= p.M) break;
-        if (p.Z) {
+        if (GATED && p.Z) {
 #pragma unroll 1
-          for (int o = 0; o < (GATED ? 2 : 1); ++o) {
+          for (int o = 0; o < 2; ++o) {
             uint8_t *slot = slots + (used++ & 1) * PSLOT;
             slot_free<false>(lane);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
               float v[32];
               tmem_ld32(tq + cc + NB / 2 * o + 32 * h, v);
-              if (!GATED && p.bias) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  v[k] += col + 32 * h + k < p.N ? __ldg(p.bias + col + 32 * h + k) : 0.f;
-              }
               stage32(slot, lane, h, v);
             }
             slot_out(o ? &out.z2 : &out.z, o ? p.Z2 : p.Z, p.ldz, p.M, p.N, slot, lane, col, row0);
           }
         }
+        // (Z of a linear product goes out beside Y, through the other slot)
+        const bool keep = !GATED && p.Z;
+        uint8_t *zslot = slots + (used & 1) * PSLOT;
+        if (keep) {
+          ++used;
+          slot_free<true>(lane);
+        }
         uint8_t *slot = slots + (used++ & 1) * PSLOT;
         if (!early || c > 0) {
-          slot_free<false>(lane);
+          if (!keep) slot_free<false>(lane);
           if (!GATED && p.R) residual(slot, col);
         }
 #pragma unroll 1
@@ -723,24 +735,18 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           float v[32], u[GATED ? 32 : 1];
           tmem_ld32(tq + cc + 32 * h, v);
           if constexpr (GATED) tmem_ld32(tq + cc + NB / 2 + 32 * h, u);
-          if (!GATED && p.bias) {
+          if constexpr (!GATED) {
+            if (p.bias) {
+              float bl = bias[0];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              v[k] += col + 32 * h + k < p.N ? __ldg(p.bias + col + 32 * h + k) : 0.f;
-          }
-          if constexpr (ACT == KRONQ_ACT_GELU) {   // (long: one copy of its code)
+              for (int k = 1; k < BREGS; ++k) bl = 2 * c + h == k ? bias[k] : bl;
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 g = gelu4(make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]));
-              v[k] = g.x;
-              v[k + 1] = g.y;
-              v[k + 2] = g.z;
-              v[k + 3] = g.w;
+              for (int k = 0; k < 32; ++k) v[k] += __shfl_sync(0xffffffffu, bl, k);
             }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = act_f<ACT>(v[k]);
           }
+          if (keep) stage32(zslot, lane, h, v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = act_f<ACT>(v[k]);
           if constexpr (GATED) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) v[k] *= u[k];
@@ -754,6 +760,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
           }
           stage32(slot, lane, h, v);
         }
+        if (keep) slot_out(&out.z, p.Z, p.ldz, p.M, p.N, zslot, lane, col, row0);
         slot_out(&out.y, p.Y, p.ldy, p.M, p.N, slot, lane, col, row0);
       }
       tc_fence_before();
