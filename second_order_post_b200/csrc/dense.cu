@@ -65,11 +65,11 @@ __device__ __forceinline__ void load_panel(uint8_t *dst, const CUtensorMap *map,
 // 4096 -> 4096 7.3 us (4.6 TB/s: start, the clusters' meeting and the end cost 3 us).
 constexpr int FTHREADS = 128;
 
-template <bool GATED, int NT>
+template <bool GATED, int NT, bool TWO>
 struct Few {
   static constexpr int STAGE = DPANEL * (GATED ? 2 : 1) + NT * 128;
-  // two CTAs an SM where four stages fit in half of it, else one
-  static constexpr int PER_SM = STAGE * 4 <= 108 * 1024 ? 2 : 1;
+  // two CTAs an SM where four stages fit in half of it (TWO: three), else one
+  static constexpr int PER_SM = TWO || STAGE * 4 <= 108 * 1024 ? 2 : 1;
   static constexpr int STAGES = (PER_SM == 2 ? 108 : 216) * 1024 / STAGE;
   static constexpr int SMEM = STAGES * STAGE + 1024 + 256;
   static constexpr int COLS = (GATED ? 2 : 1) * NT < 32 ? 32 : (GATED ? 2 : 1) * NT;
@@ -121,12 +121,12 @@ __device__ __forceinline__ void finish4(const DenseP &p, int64_t row, int64_t co
   store4(p.Y + row * p.ldy + col, v, n);
 }
 
-template <bool GATED, bool W_MN, int NT>
-__global__ void __launch_bounds__(FTHREADS, Few<GATED, NT>::PER_SM)
+template <bool GATED, bool W_MN, int NT, bool TWO>
+__global__ void __launch_bounds__(FTHREADS, Few<GATED, NT, TWO>::PER_SM)
     dense_few_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmX2,
                      const __grid_constant__ CUtensorMap tmW2, const FewP fp) {
-  using C = Few<GATED, NT>;
+  using C = Few<GATED, NT, TWO>;
   const DenseP &p = fp.d;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -1000,10 +1000,10 @@ int resident_clusters(int per_sm, int n) {
 // 9.7 us in six parts and 13.9 in seven, of which 34 clusters are on the chip. Five
 // to seven parts pay for one tile of 16 tokens only: 64 tokens 4096 -> 6016 take 17.8
 // in five, 14.7 in four (the sums of the parts are shared out evenly over four).
-template <bool GATED, bool W_MN, int NT>
+template <bool GATED, bool W_MN, int NT, bool TWO = false>
 kronq_status launch_few(cudaStream_t st, const CUtensorMap *tm, const DenseP &d, int act) {
-  using C = Few<GATED, NT>;
-  auto *kern = dense_few_kernel<GATED, W_MN, NT>;
+  using C = Few<GATED, NT, TWO>;
+  auto *kern = dense_few_kernel<GATED, W_MN, NT, TWO>;
   KQ_TRY(smem_attr(kern, C::SMEM));
   FewP p;
   p.d = d;
@@ -1131,7 +1131,12 @@ kronq_status tokens_product(cudaStream_t st, const Operands &o, const DenseP &p,
     case 32: return launch_few<GATED, W_MN, 32>(st, tm, p, act);
     case 64: return launch_few<GATED, W_MN, 64>(st, tm, p, act);
   }
-  if constexpr (!GATED) return launch_few<GATED, W_MN, 128>(st, tm, p, act);
+  // 128 tokens a tile: above 45 tiles one CTA an SM leaves too little to split. With
+  // one | two an SM: 128 tokens 4096 -> 4096 12.9 | 14.8 us, 5120 15.4 | 17, 7424 19.9 |
+  // 18.8, 11008 28.6 | 23.9.
+  if constexpr (!GATED)
+    return ceil_div(p.N, DT) > 45 ? launch_few<GATED, W_MN, 128, true>(st, tm, p, act)
+                                  : launch_few<GATED, W_MN, 128>(st, tm, p, act);
   return KRONQ_ERR_UNSUPPORTED;   // (not reached)
 }
 

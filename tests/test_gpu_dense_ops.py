@@ -76,6 +76,16 @@ def test_linear_many_and_few_tiles(cuda_device, size):
     test_gated_bwd(cuda_device, size, "silu")
 
 
+@pytest.mark.parametrize("size", [(100, 4104, 300), (128, 4096, 1000), (77, 4100, 6020),
+                                  (5, 4100, 5100), (48, 640, 4700), (20, 900, 9001)])
+def test_few_tokens_many_parts(cuda_device, size):
+    """Few tokens: long rows up to 128 tokens, and column tiles of which a part more
+    than the chip holds at once would be needed."""
+    test_linear(cuda_device, size, "gelu_tanh")
+    test_linear_bwd(cuda_device, size, "silu")
+    test_gated(cuda_device, size, "silu")
+
+
 @pytest.mark.parametrize("size", [(4500, 72, 1027), (5000, 40, 1089)])
 def test_last_columns_alone_in_their_slot(cuda_device, size):
     """Several tiles a CTA, the last block of 64 columns fewer than eight wide: the
