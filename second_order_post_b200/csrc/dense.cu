@@ -682,7 +682,10 @@ __global__ void __launch_bounds__(PTHREADS, 1)
       constexpr int SLOTS = NT / 64, FIRST = (SLOTS + 1) / 2;
       const int mine = half == 0 ? FIRST : SLOTS - FIRST, first = half * FIRST * 64;
       const bool busy = mine > 0;
-      const bool early = !GATED && busy && p.R && !p.Z;   // the first output takes R
+      // The first output takes R. Only if there is one: what lies outside the
+      // matrix is left without waiting for its copies, and those of the next tile
+      // to the same slot are not ordered behind them.
+      const bool early = !GATED && busy && p.R && !p.Z && bj * NT + first < p.N && row0 < p.M;
       if (early) {
         slot_free<false>(lane);
         residual(slots + (used & 1) * PSLOT, bj * NT + first);

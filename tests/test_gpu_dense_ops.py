@@ -95,6 +95,29 @@ def test_last_columns_alone_in_their_slot(cuda_device, size):
     test_gated(cuda_device, size, "relu")
 
 
+@pytest.mark.parametrize("size", [(4500, 72, 1089), (5000, 40, 1056), (9700, 64, 300),
+                                  (4097, 136, 1290)])
+def test_residual_with_tiles_partly_outside(cuda_device, size):
+    """Several tiles a CTA, the last of a row and of a column with warps whose rows
+    or columns lie outside the matrix: their staging slots hold the next tile's
+    residual values all the same."""
+    K = kq()
+    n, d_in, d_out = size
+    X, W = matrix(n, d_in, 1), matrix(d_out, d_in, 2, 1.3 / math.sqrt(d_in))
+    R, info = matrix(n, d_out, 3, 2.0, pad=1), _info()
+    x, w = X.double(), W.double()
+    y = x @ w.T + R.double()
+    e = acc_bound(x, w) + U32 * y.abs()
+    tol = e + HALF_BF16 * (y.abs() + e) + 1e-30
+    for _ in range(5):
+        Y, ybuf = out_like(n, d_out, pad=1)
+        K.kronq_linear(X, W, Y, info, R=R)
+        torch.cuda.synchronize()
+        assert info.item() == 0
+        close(Y, y, tol)
+        assert untouched(ybuf, d_out)
+
+
 def test_linear_in_place_residual(cuda_device):
     K = kq()
     n, d_in, d_out = 300, 256, 392
