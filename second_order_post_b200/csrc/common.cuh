@@ -119,6 +119,8 @@ inline kronq_status launch_kernel(cudaStream_t st, void (*kern)(P...), int64_t g
 // ----------------------------------------------------------------- device side
 // Waits until the kernels before this one on the stream have completed and
 // their writes are visible (at once if the kernel was not launched early).
+// Behind it their results are read by plain loads: the read-only path wants data
+// that nothing writes while the kernel lives, and it lives beside their last CTAs.
 __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(PTHREADS, 1)
 #pragma unroll
         for (int k = 0; k < BREGS; ++k) {
           const int64_t col = bj * NT + first + 32 * k + lane;
-          bias[k] = p.bias && k < 2 * mine && col < p.N ? __ldg(p.bias + col) : 0.f;
+          bias[k] = p.bias && k < 2 * mine && col < p.N ? p.bias[col] : 0.f;
         }
       }
       const bool ok = mbar_wait(&ctl->tfull[a], (i >> 1) & 1, abort);

@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(ST, 1024 / ST)
 #pragma unroll
     for (int u = 0; u < FWD_U; ++u) {
       const int64_t at = v + u * ST;
-      x[u] = at < w1 ? __ldg(zv + at) : neg_inf_vec<T>();
+      x[u] = at < w1 ? zv[at] : neg_inf_vec<T>();
     }
   };
   uint4 x[FWD_U];

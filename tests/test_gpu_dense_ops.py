@@ -426,6 +426,41 @@ def test_captured_and_replayed(cuda_device):
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+def test_each_call_reads_what_the_one_before_wrote(cuda_device):
+    """Calls one behind the other on a stream, launched while the one before drains:
+    a bias made by a backward pass, logits made by a product, a loss of them."""
+    K = kq()
+    n, d, f, vocab = 384, 128, 640, 5001
+    W, Wh, info = matrix(f, d, 1, 0.1), matrix(vocab, f, 2, 0.05), _info()
+    ones = matrix(n, f, 3)
+    T = torch.randn(n, 4, generator=torch.Generator().manual_seed(4)).cuda()
+    idx = torch.randint(0, vocab, (n, 4), generator=torch.Generator().manual_seed(5)).int().cuda()
+    Xs = [matrix(n, d, 10 + j) for j in range(6)]
+    dYs = [matrix(n, f, 20 + j, 0.1) for j in range(6)]
+    db = torch.zeros(f, device="cuda")
+    Y, logits = out_like(n, f)[0], out_like(n, vocab)[0]
+
+    def chain(j, sync):
+        loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        K.kronq_linear_bwd(dYs[j], Xs[j], None, info, act=K.KRONQ_ACT_RELU, Z=ones,
+                           dZ=dYs[j].clone(), db=db)
+        sync()
+        K.kronq_linear(Xs[j], W, Y, info, bias=db, act=K.KRONQ_ACT_SILU)
+        sync()
+        K.kronq_linear(Y, Wh, logits, info)
+        sync()
+        K.kronq_distill_fwd(logits, T, idx, loss, lse, info)
+        sync()
+        return loss, lse
+
+    want = [chain(j, torch.cuda.synchronize) for j in range(6)]
+    for _ in range(10):
+        got = [chain(j, lambda: None) for j in range(6)]
+        torch.cuda.synchronize()
+        assert info.item() == 0
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+
+
 def test_two_streams_at_once(cuda_device):
     """Calls that overlap on the GPU (large and small products, distillation,
     a covariance) share nothing: each gives what it gives alone."""
