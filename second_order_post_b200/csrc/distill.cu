@@ -30,7 +30,7 @@ struct DistillP {
   int64_t vocab, ldz, ldt, lddz;
   const int32_t *idx;
   int k, t_bf16;
-  float c_hi, c_lo, tau;   // c = log2(e) / tau in two parts
+  float c, tau;            // c = log2(e) / tau
   double inv_tau;
   const float *weight;
   float *loss, *lse;
@@ -49,20 +49,27 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// 2^(z c - b) with b in two parts
-template <class T>
-__device__ __forceinline__ float exp_term(float z, float c_hi, float c_lo, float b_hi, float b_lo) {
-  float a;
-  if constexpr (sizeof(T) == 4) {
-    z = max_nan(z, -3.0e38f);   // -inf * c_lo has no place in a sum
-    a = fmaf(z, c_hi, -b_hi) + fmaf(z, c_lo, -b_lo);
-  } else {
-    a = fmaf(z, c_hi, -b_hi);
-  }
+__device__ __forceinline__ float ex2(float a) {
   float e;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a));
   return e;
 }
+
+// exp((z - m) / tau) = 2^((z - m) c). The difference comes first, so that its
+// rounding is relative to it: in z c - m c the rounding of m c alone is 2^-25 |m c|
+// in the exponent, which has no bound over the logits and temperatures allowed (with
+// |m| / tau = 1e8 the sum of a row came out negative). It costs an addition a pair.
+//   shift: added to the exponent (0 with m from the row's own logits).
+struct Exponent {
+  F2 c, b, d;
+  __device__ __forceinline__ Exponent(float m, float c1, float shift = 0.f)
+      : c(f2(c1, c1)), b(f2(-m, -m)), d(f2(shift, shift)) {}
+  __device__ __forceinline__ F2 operator()(F2 z) const {
+    const float2 x = f2_get(f2_fma(f2_add(z, b), c, d));
+    return f2(ex2(x.x), ex2(x.y));
+  }
+  __device__ __forceinline__ float one(float z) const { return f2_get((*this)(f2(z, z))).x; }
+};
 
 // Block reductions in a fixed order; every thread gets the result.
 template <class V, class F>
@@ -127,20 +134,21 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
 
   // ---- log-sum-exp of the row
   double lse;
+  float m = -INFINITY, s = 0.f, shift = 0.f;
   if (FWD) {
-    float m = -INFINITY;
     for (int64_t v = tid; v < a.vocab; v += DI_THREADS) m = max_nan(m, to_f(z[v]));
     m = block_reduce(m, red, -INFINITY, [](float x, float y) { return max_nan(x, y); });
-    const double mc = double(m) * (double(a.c_hi) + double(a.c_lo));
-    const float b_hi = float(mc), b_lo = float(mc - double(b_hi));
-    float s = 0.f;
-    for (int64_t v = tid; v < a.vocab; v += DI_THREADS)
-      s += exp_term<T>(to_f(z[v]), a.c_hi, a.c_lo, b_hi, b_lo);
+    if (m < NO_LOGIT) m = NAN;   // no logit at all: q has no value
+    const Exponent ex(m, a.c);
+    for (int64_t v = tid; v < a.vocab; v += DI_THREADS) s += ex.one(to_f(z[v]));
     s = block_reduce(s, red, 0.f, add);
     lse = double(m) / double(a.tau) + log(double(s));
-    if (m < NO_LOGIT) lse = double(NAN);
   } else {
+    // relative to tau lse; what fp32 drops of it goes into the exponent
     lse = a.lse[row];
+    const double r = lse * double(a.tau);
+    m = float(r);
+    shift = float((double(m) - r) * double(a.c));
   }
 
   // ---- loss; p_s becomes p
@@ -164,19 +172,18 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
   }
 
   // ---- gradient
-  const double L = lse * 1.4426950408889634074;
-  const float b_hi = float(L), b_lo = float(L - double(b_hi));
-  const float wt = w * a.tau;
+  const Exponent ex(m, a.c, shift);
+  const float wt = w * a.tau, scale = FWD ? __fdiv_rn(wt, s) : wt;
   __syncthreads();
   for (int64_t v = tid; v < a.vocab; v += DI_THREADS)
-    put(dz + v, wt * exp_term<T>(to_f(z[v]), a.c_hi, a.c_lo, b_hi, b_lo));
+    put(dz + v, scale * ex.one(to_f(z[v])));
   __syncthreads();
   for (int j = tid; j < a.k; j += DI_THREADS) {
     const int32_t i = i_s[j];
     if (i < 0) continue;
     float p = 0.f;
     for (int l = 0; l < a.k; ++l) p += i_s[l] == i ? p_s[l] : 0.f;
-    put(dz + i, wt * (exp_term<T>(z_s[j], a.c_hi, a.c_lo, b_hi, b_lo) - p));
+    put(dz + i, scale * ex.one(z_s[j]) - wt * p);
   }
 }
 
@@ -213,36 +220,6 @@ __device__ __forceinline__ void store_vec2(__nv_bfloat16 *p, const F2 *x) {
   }
   *reinterpret_cast<uint4 *>(p) = o;
 }
-
-__device__ __forceinline__ float ex2(float a) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a));
-  return e;
-}
-
-// 2^((z - m) c) of a pair. fp32: the difference first, so that its rounding is
-// relative to it. bf16: z c - m c in one step, relative to m c as rounded; the
-// rounding is a factor 1 + fix for all values with this m.
-template <class T>
-struct Exponent {
-  F2 c, b;
-  float fix;
-  __device__ __forceinline__ Exponent(float m, float c1) {
-    c = f2(c1, c1);
-    if constexpr (sizeof(T) == 4) {
-      b = f2(-m, -m);
-      fix = 0.f;
-    } else {
-      const float mc = m * c1;
-      b = f2(-mc, -mc);
-      fix = -0.69314718f * fmaf(m, c1, -mc);
-    }
-  }
-  __device__ __forceinline__ F2 operator()(F2 z) const {
-    const float2 x = f2_get(sizeof(T) == 4 ? f2_mul(f2_add(z, b), c) : f2_fma(z, c, b));
-    return f2(ex2(x.x), ex2(x.y));
-  }
-};
 
 // (m, s) pairs: m may be -inf (then s is 0)
 __device__ __forceinline__ float rescale(float s, float from, float to, float c) {
@@ -380,7 +357,7 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
   const bool clus = FWD && parts > 1;
   const int rank = blockIdx.x % parts, vocab = static_cast<int>(a.vocab), k = a.k;
   const int stride = gridDim.x / parts;
-  const float c2e = a.c_hi;
+  const float c2e = a.c;
   const int lw = kq_min(WARPS, (k + 31) / 32);   // warps with teacher entries
   if (tid == 0) {
     mbar_init(&bar, 1);
@@ -493,7 +470,7 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
 #pragma unroll 4
         for (int v = tid; v < cnt; v += ST) m = max_nan(m, max_vec<T>(buf[v]));
         m = m < NO_LOGIT ? NO_LOGIT : m;    // exponents of masked logits: -inf
-        const Exponent<T> ex(m, a.c_hi);
+        const Exponent ex(m, c2e);
         F2 acc0 = f2(0.f, 0.f), acc1 = acc0;
 #pragma unroll 4
         for (int v = tid; v < cnt; v += ST) {
@@ -507,7 +484,6 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
         }
         const float2 sum = f2_get(f2_add(acc0, acc1));
         s = sum.x + sum.y;
-        s = fmaf(s, ex.fix, s);
         warp_pair(m, s, c2e);
       }
     }
@@ -542,12 +518,11 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
     if (!FWD) {
       const double r = double(lse_in) * double(a.tau);
       ref = float(r);
-      fix = -0.69314718f * a.c_hi * float(r - double(ref));
+      fix = -0.69314718f * c2e * float(r - double(ref));
     }
     scale = FWD ? __fdiv_rn(wt, s) : wt;
-    const Exponent<T> ex(ref, a.c_hi);
-    fix += ex.fix;
-    scale = fmaf(scale, fix, scale);
+    const Exponent ex(ref, c2e);
+    if (!FWD) scale = fmaf(scale, fix, scale);
     T *dz = static_cast<T *>(a.dZ) + int64_t(row) * a.lddz;
     const bool vec =
         (reinterpret_cast<uintptr_t>(dz) & 15) == (reinterpret_cast<uintptr_t>(z) & 15);
@@ -597,7 +572,7 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
           y += double(p);
         }
         tr[j] = wt * p;
-        zr[j] = scale * f2_get(ex(f2(zj, zj))).x;
+        zr[j] = scale * ex.one(zj);
       }
       if (FWD && rank == 0) {
         __syncwarp();
@@ -671,7 +646,7 @@ __global__ void __launch_bounds__(ST, 1024 / ST)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % parts, k = a.k;
   const int64_t row = blockIdx.x / parts;
-  const float c2e = a.c_hi;
+  const float c2e = a.c;
   pdl_launch();
   pdl_wait();
   const float w = a.weight ? a.weight[row] : 1.f;
@@ -700,7 +675,7 @@ __global__ void __launch_bounds__(ST, 1024 / ST)
       s = rescale(s, m, top, c2e);
       m = top;
     }
-    const Exponent<T> ex(m, c2e);
+    const Exponent ex(m, c2e);
     F2 acc0 = f2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
     for (int u = 0; u < FWD_U; ++u) {
@@ -713,7 +688,7 @@ __global__ void __launch_bounds__(ST, 1024 / ST)
       }
     }
     const float2 sum = f2_get(f2_add(acc0, acc1));
-    s += fmaf(sum.x + sum.y, ex.fix, sum.x + sum.y);
+    s += sum.x + sum.y;
   };
   auto load = [&](int64_t v, uint4 *x) {
 #pragma unroll
@@ -964,9 +939,7 @@ kronq_status distill(cudaStream_t st, const DistillArgs &a) {
   p.idx = a.idx;
   p.k = a.k;
   p.t_bf16 = a.t_bf16;
-  const double c = 1.4426950408889634074 / double(a.tau);
-  p.c_hi = float(c);
-  p.c_lo = float(c - double(p.c_hi));
+  p.c = float(1.4426950408889634074 / double(a.tau));
   p.tau = a.tau;
   p.inv_tau = 1.0 / double(a.tau);
   p.weight = a.weight;

@@ -273,6 +273,97 @@ def test_large_logits_and_temperatures(cuda_device):
               + 8 * U32 * float(w.max()) * tau)
 
 
+def _far(Z, T, idx, tau, w):
+    """What _step gives and its bounds, from differences to the row's maximum: lse
+    itself may be too large to subtract, even in fp64."""
+    z, m = Z.double(), Z.double().amax(1, keepdim=True)
+    d = (z - m) / tau
+    ls = d.exp().sum(1)
+    logq = d - ls.log()[:, None]
+    q = logq.exp()
+    at = idx.long()
+    p = torch.softmax(T.double() / tau, 1)
+    terms = torch.where(p > 0, p * (p.log() - logq.gather(1, at)), 0.0)
+    loss = tau ** 2 * terms.sum(1)
+    lse = m[:, 0] / tau + ls.log()
+    dz = w.double()[:, None] * tau * q.scatter_add(1, at, -p)
+    none = torch.zeros_like(lse)   # (the step does not go through a stored lse)
+    b_loss, b_lse, b_dz = _bounds(Z, T, idx, tau, w, (loss, none, dz, q, p, logq, None))
+    # the loss adds and subtracts the maximum in fp64
+    return (loss, lse, dz), (b_loss + tau ** 2 * 2.0 ** -48 * (m[:, 0] / tau).abs(),
+                             b_lse + 2 * U32 * lse.abs(), b_dz)
+
+
+def _check_far(Z, T, idx, tau, w):
+    K = kq()
+    want, b = _far(Z, T, idx, tau, w)
+    loss, lse, dZ, info = _run(Z, T, idx, tau, w, True)
+    assert info == 0
+    close(loss, want[0], b[0])
+    close(lse, want[1], b[1])
+    close(dZ, want[2], b[2])
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    K.kronq_distill_fwd(Z, T, idx, loss, lse, info, tau=tau, weight=w)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    close(loss, want[0], b[0])
+    close(lse, want[1], b[1])
+
+
+# rows of every kernel: 64, 128 and 384 threads, clusters, no cluster holds them
+FAR_WIDTHS = [600, 9001, 20000, 70003, 300001]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", FAR_WIDTHS)
+@pytest.mark.parametrize("mask", [-1e9, -1e10, -1e20, -1e30])
+def test_finite_masks(cuda_device, dtype, vocab, mask):
+    """Whole slices of a row masked by a large negative logit, at its start, at its end
+    and all but a few places: as the definition has it, which gives them nothing."""
+    n, k = 4, 6
+    Z, T, idx, w = _case(n, vocab, k, dtype, seed=vocab)
+    named = torch.zeros(n, vocab, dtype=torch.bool, device="cuda")
+    named.scatter_(1, idx.long(), True)
+    place = torch.arange(vocab, device="cuda")
+    for r, out in enumerate((place < vocab // 2, place > vocab // 3, place != 5, place % 9 > 0)):
+        Z[r, out & ~named[r]] = mask
+    for tau in (1.0, 2.5, 0.125):
+        _check_far(Z, T, idx, tau, w)
+        want = _want(Z, T, idx, tau, w)
+        b = _bounds(Z, T, idx, tau, w, want)
+        loss, lse, dZ, info = _run(Z, T, idx, tau, w, False)
+        assert info == 0
+        close(loss, want[0], b[0])
+        close(lse, want[1], b[1])
+        close(dZ, want[2], b[2])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", FAR_WIDTHS)
+def test_logits_far_from_zero(cuda_device, dtype, vocab):
+    """Rows around a value that is up to 1e10 and more temperatures from zero, of both
+    signs: one maximum, several of them, a spread of neighbours, all the same."""
+    n, k = 4, 5
+    for top, tau in ((3584.0, 1e-4), (1e5, 1e-3), (1e6, 1e-4), (3e9, 1.0), (1e10, 1.0),
+                     (1e10, 1e4), (1e20, 1e4), (4e31, 1e-4), (4e31, 1e4)):
+        tau = float(torch.tensor(tau, dtype=torch.float32))
+        for sign in (1, -1):
+            g = torch.Generator().manual_seed(vocab)
+            step = torch.finfo(dtype).eps / 2 * top
+            Z = torch.full((n, vocab), sign * top, dtype=torch.float64)
+            Z[0] -= top * torch.rand(vocab, generator=g)
+            Z[0, 77] = (sign + 0.05) * top
+            Z[1] -= 0.3 * top * (torch.arange(vocab) % 7 != 3)
+            Z[2] -= 2 * step * torch.randint(0, 6, (vocab,), generator=g)
+            Z = Z.to(dtype).cuda()
+            idx = torch.stack([torch.randperm(vocab, generator=g)[:k] for _ in range(n)]).int()
+            idx[:, 1] = 77
+            idx[:, 2] = torch.where(idx[:, 2] == 77, 78, idx[:, 2])
+            T = torch.randn(n, k, generator=g) * tau
+            w = torch.rand(n, generator=g) + 0.1
+            _check_far(Z, T.cuda(), idx.cuda(), tau, w.cuda())
+
+
 def test_gradient_against_differences(cuda_device):
     """dZ against central differences of the fp64 loss."""
     n, vocab, k, tau, h = 2, 50, 6, 1.7, 1e-4
