@@ -271,8 +271,10 @@ constexpr int wide_per_sm() {
 }
 
 // ln(x) for a normal x > 0, off by less than 4e-8: exponent times ln 2 in
-// fp64, plus the fp32 logarithm of a mantissa in [0.75, 1.5)
+// fp64, plus the fp32 logarithm of a mantissa in [0.75, 1.5). NaN for what is no
+// sum of a row that has a softmax: NaN, inf, 0 and less.
 __device__ __forceinline__ double log_split(float x) {
+  if (!(x > 0.f && x < INFINITY)) return double(NAN);
   const int ex = (__float_as_int(x) - 0x3f400000) >> 23;
   const float f = __int_as_float(__float_as_int(x) - (ex << 23));
   return double(ex) * 0.69314718055994530942 + double(logf(f));

@@ -18,6 +18,9 @@ pytestmark = pytest.mark.gpu
 SIZES = [(1, 1, 1), (2, 7, 3), (5, 33, 33), (3, 1000, 16), (2, 4099, 64), (4, 8192, 1),
          (2, 32000, 100), (2, 50257, 17), (1, 65537, 1024), (2, 128256, 64), (1, 300001, 8)]
 
+# rows of every kernel: 64, 128 and 384 threads, clusters, no cluster holds them
+FAR_WIDTHS = [600, 9001, 20000, 70003, 300001]
+
 
 def _case(n, vocab, k, dtype, seed, tdtype=torch.float32, pad=0):
     g = torch.Generator().manual_seed(seed)
@@ -217,6 +220,30 @@ def test_nonfinite_is_reported(cuda_device, dtype):
                 assert torch.equal(dZ[keep], clean[2][keep])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", FAR_WIDTHS)
+def test_infinite_logit(cuda_device, dtype, vocab):
+    """A logit of +inf, named by the teacher or not: loss (unless it is infinite), lse
+    and gradient of its row are NaN and reported, the other rows as without it."""
+    K = kq()
+    n, k = 4, 5
+    Z, T, idx, w = _case(n, vocab, k, dtype, seed=9)
+    clean = _run(Z, T, idx, 1.5, w, True)
+    for at in (0, vocab - 1, vocab // 2, int(idx[2, 1])):
+        Z2 = Z.clone()
+        Z2[2, at] = math.inf
+        for fused in (True, False):
+            loss, lse, dZ, info = _run(Z2, T, idx, 1.5, w, fused)
+            assert info == K.KRONQ_ERR_NONFINITE
+            assert not bool(loss[2].isfinite())
+            assert bool(lse[2].isnan()) and bool(dZ[2].isnan().all())
+            keep = [0, 1, 3]
+            if fused:
+                assert torch.equal(loss[keep], clean[0][keep])
+                assert torch.equal(lse[keep], clean[1][keep])
+                assert torch.equal(dZ[keep], clean[2][keep])
+
+
 def test_place_outside_the_vocabulary(cuda_device):
     """Left out like padding, and reported."""
     K = kq()
@@ -308,10 +335,6 @@ def _check_far(Z, T, idx, tau, w):
     assert info.item() == 0
     close(loss, want[0], b[0])
     close(lse, want[1], b[1])
-
-
-# rows of every kernel: 64, 128 and 384 threads, clusters, no cluster holds them
-FAR_WIDTHS = [600, 9001, 20000, 70003, 300001]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
