@@ -511,7 +511,10 @@ kronq_status kronq_gated_bwd(kronq_stream_t stream, const void *dH,
  * row's logarithms and its loss fp64, rounded once. info_dev: NONFINITE when
  * the loss of a row that counts is not finite.
  * _fwd writes loss and lse (n fp32), _bwd takes that lse and writes dZ (n x
- * vocab, zdtype), _step does both while a row is on the chip. dZ may be Z
+ * vocab, zdtype), _step does both while a row is on the chip. _bwd's q_v is
+ * exp(Z_v / tau - lse) for the lse it is given, which fp32 holds to 2^-24 of
+ * itself: a factor exp(2^-24 |lse|) of q, 1.0006 at |lse| = 1e4 and e at 1.7e7.
+ * _step has no such factor: it divides by the row's own sum. dZ may be Z
  * (the same stride). 1 <= k <= 1024, 1e-4 <= tau <= 1e4, vocab < 2^31;
  * pointers aligned to their element. Logits of up to 1e32 in magnitude; one
  * below -1e32 (a mask) counts as -inf. A row whose logits are all -inf, or that

@@ -71,6 +71,16 @@ struct Exponent {
   __device__ __forceinline__ float one(float z) const { return f2_get((*this)(f2(z, z))).x; }
 };
 
+// exp(z / tau - lse) = 2^((z - m) c + shift) for a row's stored lse: m = tau lse in
+// fp32, and shift what that drops of it, in the exponent (it is up to 2^-24 |lse|, and
+// a factor 1 + shift ln 2 would do for small ones only).
+__device__ __forceinline__ void lse_reference(float lse, const DistillP &a, float &m,
+                                              float &shift) {
+  const double r = double(lse) * double(a.tau);
+  m = float(r);
+  shift = float((double(m) - r) * double(a.c));
+}
+
 // Block reductions in a fixed order; every thread gets the result.
 template <class V, class F>
 __device__ __forceinline__ V block_reduce(V v, V *red, V zero, F f) {
@@ -144,11 +154,8 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
     s = block_reduce(s, red, 0.f, add);
     lse = double(m) / double(a.tau) + log(double(s));
   } else {
-    // relative to tau lse; what fp32 drops of it goes into the exponent
     lse = a.lse[row];
-    const double r = lse * double(a.tau);
-    m = float(r);
-    shift = float((double(m) - r) * double(a.c));
+    lse_reference(a.lse[row], a, m, shift);
   }
 
   // ---- loss; p_s becomes p
@@ -515,16 +522,11 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
     const float wt = w * a.tau;
     // The exponentials of the gradient: those of the sums, relative to the row's
     // m, over s; in the backward pass alone relative to tau lse, of which the
-    // part that fp32 drops goes into the factor.
-    float ref = m, scale = 0.f, fix = 0.f;
-    if (!FWD) {
-      const double r = double(lse_in) * double(a.tau);
-      ref = float(r);
-      fix = -0.69314718f * c2e * float(r - double(ref));
-    }
-    scale = FWD ? __fdiv_rn(wt, s) : wt;
-    const Exponent ex(ref, c2e);
-    if (!FWD) scale = fmaf(scale, fix, scale);
+    // part that fp32 drops goes into the exponent.
+    float ref = m, shift = 0.f;
+    if (!FWD) lse_reference(lse_in, a, ref, shift);
+    const float scale = FWD ? __fdiv_rn(wt, s) : wt;
+    const Exponent ex(ref, c2e, shift);
     T *dz = static_cast<T *>(a.dZ) + int64_t(row) * a.lddz;
     const bool vec =
         (reinterpret_cast<uintptr_t>(dz) & 15) == (reinterpret_cast<uintptr_t>(z) & 15);

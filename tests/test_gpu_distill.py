@@ -387,6 +387,51 @@ def test_logits_far_from_zero(cuda_device, dtype, vocab):
             _check_far(Z, T.cuda(), idx.cuda(), tau, w.cuda())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", FAR_WIDTHS)
+def test_backward_from_a_large_lse(cuda_device, dtype, vocab):
+    """The backward pass alone is exp(z / tau - lse) for the lse that it is given, also
+    where fp32 holds that no closer than to a few tens.
+    Bound: the exponent is (z - m) c + shift with m = tau lse in fp32; z - m and its
+    product with c are off by 3 2^-24 of at most |arg| + |shift|, |shift| <= 2^-24 |lse|
+    log2(e); fp64 keeps tau lse to 2^-53."""
+    K = kq()
+    n, k = 4, 5
+    for top, tau in ((1e5, 1e-2), (3584.0, 1e-4), (1e5, 1e-3), (2e12, 1e4), (3e4, 1e-4),
+                     (1e9, 1.0)):
+        tau = float(torch.tensor(tau, dtype=torch.float32))
+        for sign in (1, -1):
+            g = torch.Generator().manual_seed(vocab)
+            Z = torch.full((n, vocab), sign * top, dtype=torch.float64)
+            Z -= torch.finfo(dtype).eps * top * torch.randint(0, 4, (n, vocab), generator=g)
+            Z[0] -= 0.2 * top * (torch.arange(vocab) % 50 != 3)
+            Z = Z.to(dtype).cuda()
+            idx = torch.stack([torch.randperm(vocab, generator=g)[:k] for _ in range(n)])
+            idx = idx.int().cuda()
+            T = (torch.randn(n, k, generator=g) * tau).cuda()
+            w = (torch.rand(n, generator=g) + 0.1).cuda()
+            z, m = Z.double(), Z.double().amax(1, keepdim=True)
+            lse = (m[:, 0] / tau + ((z - m) / tau).exp().sum(1).log()).float()
+            dZ, info = torch.empty_like(Z), torch.zeros(1, dtype=torch.int32, device="cuda")
+            K.kronq_distill_bwd(Z, T, idx, lse, dZ, info, tau=tau, weight=w)
+            torch.cuda.synchronize()
+            assert info.item() == 0
+            logq = z / tau - lse.double()[:, None]
+            q, p = logq.exp(), torch.softmax(T.double() / tau, 1)
+            wt = (w.double() * tau)[:, None]
+            want = wt * q.scatter_add(1, idx.long(), -p)
+            big = lse.double().abs()[:, None]
+            arg = (logq.abs() + 2 * 2.0 ** -24 * big) * 1.4427
+            e_q = q * ((3 + arg.clamp_max(300)) * 2.0 ** -23 + 2.0 ** -50 * big)
+            tm = T.double().amax(1, keepdim=True)
+            e_p = p * (4 + (T.double() - tm).abs() / tau * 2) * 2.0 ** -23
+            # a q below 2^-126 is flushed to 0 before wt multiplies it: off by at most
+            # wt 2^-126 (with tau = 1e4 more than the 1e-37 of the last line)
+            e = wt * (e_q.scatter_add(1, idx.long(), e_p) + 2.0 ** -126)
+            step = HALF_BF16 if dtype == torch.bfloat16 else U32
+            close(dZ, want, e + step * (want.abs() + e) + 4 * U32 * want.abs() + 1e-37)
+
+
 def test_gradient_against_differences(cuda_device):
     """dZ against central differences of the fp64 loss."""
     n, vocab, k, tau, h = 2, 50, 6, 1.7, 1e-4
