@@ -46,6 +46,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+// a logit at a place that the teacher names: its distance to the maximum enters the
+// loss (in the sums the exponentials of what lies below are 0 as they are)
+__device__ __forceinline__ float named_logit(float z) { return z < NO_LOGIT ? -INFINITY : z; }
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
       if (!in) t = -INFINITY;
       i_s[j] = in && t != -INFINITY ? i : -1;
       p_s[j] = t;
-      z_s[j] = in ? to_f(z[i]) : 0.f;
+      z_s[j] = in ? named_logit(to_f(z[i])) : 0.f;
       any |= t != -INFINITY;
       tmax = fmaxf(tmax, t);
     }
@@ -456,6 +459,7 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
           entry(row, j, i, t);
           zj = to_f(logit_at(row, i));
         }
+        zj = named_logit(zj);
         if (i >= vocab) report(a.info, KRONQ_ERR_INVALID_ARG);
         if (i < 0 || i >= vocab) t = -INFINITY;
         if (t == -INFINITY) i = -1;
@@ -716,7 +720,7 @@ __global__ void __launch_bounds__(ST, 1024 / ST)
       const bool in = i >= 0 && i < a.vocab;
       if (!in) t = -INFINITY;
       t_s[j] = t;
-      z_s[j] = in ? to_f(z[i]) : 0.f;
+      z_s[j] = in ? named_logit(to_f(z[i])) : 0.f;
       const float m2 = max_nan(tm, t);
       ts = rescale(ts, tm, m2, c2e) + (t == -INFINITY ? 0.f : ex2((t - m2) * c2e));
       tm = m2;

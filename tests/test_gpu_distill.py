@@ -363,6 +363,29 @@ def test_finite_masks(cuda_device, dtype, vocab, mask):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("vocab", FAR_WIDTHS)
+def test_masks_below_the_border(cuda_device, dtype, vocab):
+    """A logit below -1e32 is -inf wherever it stands: at a place that the teacher
+    names the loss is infinite and reported, and the gradient is that of -inf."""
+    K = kq()
+    n, k = 4, 5
+    Z, T, idx, w = _case(n, vocab, k, dtype, seed=vocab + 1)
+    place = torch.arange(vocab, device="cuda")
+    for low in (-1.1e32, -1e35, torch.finfo(dtype).min):
+        for tau in (0.5, 4.0):
+            A, B = Z.clone(), Z.clone()
+            named = torch.zeros(n, vocab, dtype=torch.bool, device="cuda")
+            named.scatter_(1, idx.long(), True)
+            out = (place < vocab // 2)[None, :] & ~named
+            out[2, idx[2, 1]] = True
+            A[out], B[out] = low, -math.inf
+            for fused in (True, False):
+                got, want = (_run(t, T, idx, tau, w, fused) for t in (A, B))
+                assert got[3] == want[3] == K.KRONQ_ERR_NONFINITE and got[0][2] == math.inf
+                assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", FAR_WIDTHS)
 def test_logits_far_from_zero(cuda_device, dtype, vocab):
     """Rows around a value that is up to 1e10 and more temperatures from zero, of both
     signs: one maximum, several of them, a spread of neighbours, all the same."""
