@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
       m = warp_max_nan(x.x);
       s = warp_sum(rescale(x.y, x.x, m, c2e));
     }
-    if (FWD && m <= NO_LOGIT) m = NAN;   // no logit at all: q has no value
+    if (FWD && s == 0.f) m = NAN;   // no logit at all: q has no value
     // ---- the dense gradient
     const float wt = w * a.tau;
     // The exponentials of the gradient: those of the sums, relative to the row's
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(ST, 1024 / ST)
     if (lane == 0) loss_s[warp] = make_double2(x0, y0);
     __syncthreads();
     if (tid == 0) {
-      if (m <= NO_LOGIT) m = NAN;   // no logit at all: q has no value
+      if (s == 0.f) m = NAN;   // no logit at all: q has no value
       finish_loss(a, row, counts, m, s, ts, loss_s, kq_min(WARPS, (k + 31) / 32));
     }
   }

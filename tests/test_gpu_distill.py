@@ -384,6 +384,21 @@ def test_masks_below_the_border(cuda_device, dtype, vocab):
                 assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
 
 
+@pytest.mark.parametrize("vocab", FAR_WIDTHS)
+def test_logits_at_the_border(cuda_device, vocab):
+    """-1e32 itself is a logit: a row of nothing above it has a softmax over the
+    places that hold it."""
+    n, k = 3, 4
+    Z, T, idx, w = _case(n, vocab, k, torch.float32, seed=vocab + 2)
+    Z[:] = -1e32
+    named = torch.zeros(n, vocab, dtype=torch.bool, device="cuda")
+    named.scatter_(1, idx.long(), True)
+    Z[1, ~named[1] & (torch.arange(vocab, device="cuda") % 3 == 0)] = -math.inf
+    Z[2, ~named[2]] = -2e32
+    T = torch.randn(n, k, generator=torch.Generator().manual_seed(vocab)).cuda()
+    _check_far(Z, T, idx, 2.0, w)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("vocab", FAR_WIDTHS)
 def test_logits_far_from_zero(cuda_device, dtype, vocab):
