@@ -18,7 +18,8 @@ tokens, and enqueues on one CUDA stream, per batch:
             down (dY)                            kronq_accum_cov
 
 The weights are not updated: no weight gradient is formed. All arithmetic runs
-in the library's kernels; this module only allocates and passes pointers.
+in the library's kernels; this module allocates, passes pointers and keeps the
+status words of all batches together.
 """
 from __future__ import annotations
 
@@ -57,9 +58,11 @@ class FeedForwardCalibration:
         self.H_G = {"gate": torch.empty(f, f, **f32), "up": torch.empty(f, f, **f32),
                     "down": torch.empty(d, d, **f32)}
         # status words: the block's products and loss (written on failure only,
-        # cleared here), then the five covariances
+        # cleared here), then the first failures of the five covariances, whose
+        # calls clear the word they are given
         self.info = torch.zeros(1, dtype=torch.int32, device=dev)
         self.cov_info = torch.zeros(5, dtype=torch.int32, device=dev)
+        self._batch_info = torch.zeros(5, dtype=torch.int32, device=dev)
         self._first = True
 
     def step(self, X, T, idx, weight=None, stream=None):
@@ -88,7 +91,10 @@ class FeedForwardCalibration:
         sums = ((X, self.H_X["mlp"]), (H, self.H_X["down"]), (A, self.H_G["gate"]),
                 (U, self.H_G["up"]), (dY, self.H_G["down"]))
         for i, (rows, cov) in enumerate(sums):
-            K.kronq_accum_cov(rows, cov, 1.0 / self.tokens, beta, self.cov_info[i:i + 1], stream)
+            K.kronq_accum_cov(rows, cov, 1.0 / self.tokens, beta, self._batch_info[i:i + 1],
+                              stream)
+        with torch.cuda.stream(stream):
+            self.cov_info.add_(self._batch_info * (self.cov_info == 0))
         return loss, dX
 
     def covariances(self, sublayer):

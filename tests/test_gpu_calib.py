@@ -185,3 +185,30 @@ def test_on_another_stream_and_refusals(cuda_device):
     with pytest.raises(K.KronqError) as err:      # the loss of that token
         cal.check_info()
     assert err.value.status == K.KRONQ_ERR_NONFINITE
+
+
+def test_failure_of_an_early_batch_is_reported(cuda_device, monkeypatch):
+    """A covariance's status of the first of two batches is there after the second
+    (the library's wait that runs out stands for a pipeline's)."""
+    K = kq()
+    from second_order_post_b200.calib import FeedForwardCalibration
+    d, f, vocab, n = 128, 128, 100, 16
+    cal = FeedForwardCalibration(*_block(d, f, vocab, seed=80), max_tokens=n, tokens=2 * n)
+    accum, done = K.kronq_accum_cov, []
+
+    def second_fails(A, H, alpha, beta, info, stream=None):
+        accum(A, H, alpha, beta, info, stream)
+        done.append(1)
+        if len(done) == 2:
+            K.kronq_selftest_timeout(1000, info, stream)
+
+    monkeypatch.setattr(K, "kronq_accum_cov", second_fails)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for seed in (1, 2):
+        cal.step(*_batch(n, d, vocab, 4, seed), stream=side)
+    torch.cuda.synchronize()
+    assert len(done) == 10
+    with pytest.raises(K.KronqError) as err:
+        cal.check_info()
+    assert err.value.status == K.KRONQ_ERR_TIMEOUT
