@@ -54,19 +54,31 @@ class FeedForwardCalibration:
         # rows of logits start on 16-byte boundaries, as kronq_linear wants them
         self._logits = torch.empty(n, (vocab + 7) // 8 * 8, **bf)[:, :vocab]
         self._loss = torch.empty(n, **f32)
-        self.H_X = {"mlp": torch.empty(d, d, **f32), "down": torch.empty(f, f, **f32)}
-        self.H_G = {"gate": torch.empty(f, f, **f32), "up": torch.empty(f, f, **f32),
-                    "down": torch.empty(d, d, **f32)}
+        # sums over the batches since the last reset
+        self.H_X = {"mlp": torch.zeros(d, d, **f32), "down": torch.zeros(f, f, **f32)}
+        self.H_G = {"gate": torch.zeros(f, f, **f32), "up": torch.zeros(f, f, **f32),
+                    "down": torch.zeros(d, d, **f32)}
         # status words: the block's products and loss (written on failure only,
         # cleared here), then the first failures of the five covariances, whose
         # calls clear the word they are given
         self.info = torch.zeros(1, dtype=torch.int32, device=dev)
         self.cov_info = torch.zeros(5, dtype=torch.int32, device=dev)
         self._batch_info = torch.zeros(5, dtype=torch.int32, device=dev)
-        self._first = True
+        # True: the next step writes over the sums instead of adding to them (if it is
+        # captured, so does every replay)
+        self._first = False
+
+    def reset(self, stream=None):
+        """Starts anew: the sums and the status words become 0, in stream order (a
+        captured step adds its tokens at every replay; a reset captured before it
+        starts each replay from 0)."""
+        self._first = False
+        with torch.cuda.stream(stream):
+            for t in (*self.H_X.values(), *self.H_G.values(), self.info, self.cov_info):
+                t.zero_()
 
     def step(self, X, T, idx, weight=None, stream=None):
-        """One batch: X (n x d bf16 tokens), the teacher's top logits T and
+        """Adds one batch to the sums: X (n x d bf16 tokens), the teacher's top logits T and
         their places idx (n x k), weight (n fp32, None: all 1). Returns the
         tokens' losses and dX, the gradient with respect to X (views that the
         next step overwrites)."""
@@ -87,12 +99,12 @@ class FeedForwardCalibration:
         K.kronq_gated_bwd(dH, A, U, None, self.Wg, self.Wu, A, U, info, act=self.act, dX=dX,
                           dXr=dY, stream=stream)
         beta = 0.0 if self._first else 1.0
-        self._first = False
         sums = ((X, self.H_X["mlp"]), (H, self.H_X["down"]), (A, self.H_G["gate"]),
                 (U, self.H_G["up"]), (dY, self.H_G["down"]))
         for i, (rows, cov) in enumerate(sums):
             K.kronq_accum_cov(rows, cov, 1.0 / self.tokens, beta, self._batch_info[i:i + 1],
                               stream)
+        self._first = False
         with torch.cuda.stream(stream):
             self.cov_info.add_(self._batch_info * (self.cov_info == 0))
         return loss, dX

@@ -1,5 +1,5 @@
 """What the calibration pass does around the library's calls: status words over
-several batches. The calls themselves are stood in for."""
+several batches, the start of the sums. The calls themselves are stood in for."""
 import pytest
 import torch
 
@@ -58,3 +58,45 @@ def test_first_failure_is_kept(monkeypatch):
     with pytest.raises(K.KronqError) as err:
         cal.check_info()
     assert err.value.status == K.KRONQ_ERR_TIMEOUT
+
+
+@pytest.fixture
+def fresh_memory_is_nan():
+    """torch.empty hands out NaN."""
+    torch.use_deterministic_algorithms(True)
+    yield
+    torch.use_deterministic_algorithms(False)
+
+
+def _sums(cal):
+    return [*cal.H_X.values(), *cal.H_G.values()]
+
+
+def test_sums_start_at_zero(monkeypatch, fresh_memory_is_nan):
+    """Before the first step, after a step that was refused on its way, and after a
+    reset, whatever was there."""
+    K = kq()
+    calls = Calls(K, monkeypatch)
+    cal, batch = _make()
+    assert all(not t.any() for t in _sums(cal))
+
+    def refuses(A, H, alpha, beta, info, stream=None):
+        calls.cov.append(beta)
+        if len(calls.cov) == 2:
+            raise K.KronqError("kronq_accum_cov", K.KRONQ_ERR_CUDA)
+
+    with monkeypatch.context() as m:
+        m.setattr(K, "kronq_accum_cov", refuses)
+        with pytest.raises(K.KronqError):
+            cal.step(*batch)
+    cal.step(*batch)
+    assert calls.cov == [1.0] * 7
+    for t in _sums(cal):
+        t.fill_(3.0)
+    cal.info.fill_(K.KRONQ_ERR_NONFINITE)
+    cal.cov_info.fill_(K.KRONQ_ERR_TIMEOUT)
+    cal.reset()
+    cal.check_info()
+    assert all(not t.any() for t in _sums(cal))
+    cal.step(*batch)
+    assert calls.cov[7:] == [1.0] * 5

@@ -212,3 +212,46 @@ def test_failure_of_an_early_batch_is_reported(cuda_device, monkeypatch):
     with pytest.raises(K.KronqError) as err:
         cal.check_info()
     assert err.value.status == K.KRONQ_ERR_TIMEOUT
+
+
+def test_captured_before_anything_ran(cuda_device):
+    """A step captured as the first one adds at every replay, also behind an eager step
+    that came between; after a reset the sums start anew."""
+    kq()
+    from second_order_post_b200.calib import FeedForwardCalibration
+    d, f, vocab, n = 128, 256, 300, 40
+    W = _block(d, f, vocab, seed=90)
+    warm, cal, want = (FeedForwardCalibration(*W, max_tokens=n, tokens=4 * n) for _ in range(3))
+    a, b = (_batch(n, d, vocab, 6, s) for s in (1, 2))
+    warm.step(*a)                # kernels are loaded before the capture
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cal.step(*a)
+
+    def same(batches):
+        want.reset()
+        for x in batches:
+            want.step(*x)
+        torch.cuda.synchronize()
+        want.check_info()
+        cal.check_info()
+        for k in want.H_X:
+            assert torch.equal(cal.H_X[k], want.H_X[k])
+        for k in want.H_G:
+            assert torch.equal(cal.H_G[k], want.H_G[k])
+
+    cal.step(*b)
+    g.replay()
+    g.replay()
+    same([b, a, a])
+    cal.reset()
+    g.replay()
+    same([a])
+    both = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(both):
+        cal.reset()
+        cal.step(*b)
+    both.replay()
+    both.replay()
+    same([b])
