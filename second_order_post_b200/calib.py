@@ -68,12 +68,22 @@ class FeedForwardCalibration:
         # captured, so does every replay)
         self._first = False
 
+    def _on(self, stream):
+        """The weights' device and the stream of a pass (None: that device's current
+        one) as the current ones, which all calls of the pass then go to."""
+        dev = self.Wg.device
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, not on {dev}")
+        return torch.cuda.stream(stream)
+
     def reset(self, stream=None):
         """Starts anew: the sums and the status words become 0, in stream order (a
         captured step adds its tokens at every replay; a reset captured before it
         starts each replay from 0)."""
         self._first = False
-        with torch.cuda.stream(stream):
+        with self._on(stream):
             for t in (*self.H_X.values(), *self.H_G.values(), self.info, self.cov_info):
                 t.zero_()
 
@@ -85,28 +95,30 @@ class FeedForwardCalibration:
         n = X.shape[0]
         if not 1 <= n <= self.max_tokens:
             raise ValueError(f"a batch has 1 to {self.max_tokens} tokens, not {n}")
+        with self._on(stream):
+            return self._enqueue(n, X, T, idx, weight)
+
+    def _enqueue(self, n, X, T, idx, weight):
         A, U, H, dH = (self._act[k][:n] for k in ("A", "U", "H", "dH"))
         Y, dY, dX = (self._res[k][:n] for k in ("Y", "dY", "dX"))
         logits, loss, info = self._logits[:n], self._loss[:n], self.info
-        K.kronq_gated(X, self.Wg, self.Wu, H, info, act=self.act, A=A, U=U, stream=stream)
-        K.kronq_linear(H, self.Wd, Y, info, R=X, stream=stream)
-        K.kronq_linear(Y, self.Wh, logits, info, stream=stream)
+        K.kronq_gated(X, self.Wg, self.Wu, H, info, act=self.act, A=A, U=U)
+        K.kronq_linear(H, self.Wd, Y, info, R=X)
+        K.kronq_linear(Y, self.Wh, logits, info)
         K.kronq_distill_step(logits, T, idx, loss, None, logits, info, tau=self.tau,
-                             weight=weight, stream=stream)
-        K.kronq_linear_bwd(logits, None, self.Wh, info, dX=dY, stream=stream)
-        K.kronq_linear_bwd(dY, None, self.Wd, info, dX=dH, stream=stream)
+                             weight=weight)
+        K.kronq_linear_bwd(logits, None, self.Wh, info, dX=dY)
+        K.kronq_linear_bwd(dY, None, self.Wd, info, dX=dH)
         # Gg and Gu take the place of A and U
         K.kronq_gated_bwd(dH, A, U, None, self.Wg, self.Wu, A, U, info, act=self.act, dX=dX,
-                          dXr=dY, stream=stream)
+                          dXr=dY)
         beta = 0.0 if self._first else 1.0
         sums = ((X, self.H_X["mlp"]), (H, self.H_X["down"]), (A, self.H_G["gate"]),
                 (U, self.H_G["up"]), (dY, self.H_G["down"]))
         for i, (rows, cov) in enumerate(sums):
-            K.kronq_accum_cov(rows, cov, 1.0 / self.tokens, beta, self._batch_info[i:i + 1],
-                              stream)
+            K.kronq_accum_cov(rows, cov, 1.0 / self.tokens, beta, self._batch_info[i:i + 1])
         self._first = False
-        with torch.cuda.stream(stream):
-            self.cov_info.add_(self._batch_info * (self.cov_info == 0))
+        self.cov_info.add_(self._batch_info * (self.cov_info == 0))
         return loss, dX
 
     def covariances(self, sublayer):
@@ -122,10 +134,10 @@ class FeedForwardCalibration:
         """BiIP, factor and OBS of one sublayer on copies of its covariances, in
         a SublayerEngine of its shape; returns the engine's QuantResult."""
         hx, hg = self.covariances(sublayer)
-        with torch.cuda.stream(stream or torch.cuda.current_stream(hx.device)):
+        with self._on(stream):
             engine.H_X.copy_(hx)
             engine.H_G.copy_(hg)
-        return engine.run_from_covariances(self.weight(sublayer), stream)
+            return engine.run_from_covariances(self.weight(sublayer))
 
     def check_info(self):
         """Raises KronqError for a status word that is not 0 (syncs)."""

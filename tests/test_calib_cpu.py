@@ -1,5 +1,8 @@
 """What the calibration pass does around the library's calls: status words over
-several batches, the start of the sums. The calls themselves are stood in for."""
+several batches, the start of the sums, the device and the stream. The calls themselves are stood in for."""
+import contextlib
+import types
+
 import pytest
 import torch
 
@@ -7,19 +10,38 @@ from ops_helpers import kq
 
 
 class Calls:
-    """Stands in for the library: writes the status words that a test asks for."""
+    """Stands in for the library: writes the status words that a test asks for. And
+    for torch's streams, which a machine without a GPU has none of: `stack` holds
+    the ones that were made current, `on` what was current at each call."""
 
     def __init__(self, K, monkeypatch):
         self.status = {}            # call -> status, by the order of covariance calls
-        self.cov, self.others = [], []
+        self.cov, self.on = [], []
         for name in ("kronq_gated", "kronq_linear", "kronq_linear_bwd", "kronq_gated_bwd",
                      "kronq_distill_step"):
-            monkeypatch.setattr(K, name, lambda *a, _n=name, **k: self.others.append((_n, a, k)))
+            monkeypatch.setattr(K, name, lambda *a, **k: self.seen(k.get("stream")))
         monkeypatch.setattr(K, "kronq_accum_cov", self.accum_cov)
+        self.stack = ["process"]
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: _stream(dev))
+        monkeypatch.setattr(torch.cuda, "stream", self.current)
+
+    @contextlib.contextmanager
+    def current(self, stream):
+        self.stack.append(stream)
+        yield
+        self.stack.pop()
+
+    def seen(self, stream):
+        self.on.append(stream or self.stack[-1])
 
     def accum_cov(self, A, H, alpha, beta, info, stream=None):
+        self.seen(stream)
         info.fill_(self.status.get(len(self.cov), 0))
         self.cov.append(beta)
+
+
+def _stream(dev, name="current"):
+    return types.SimpleNamespace(device=dev, name=name)
 
 
 def _make(n=8):
@@ -100,3 +122,39 @@ def test_sums_start_at_zero(monkeypatch, fresh_memory_is_nan):
     assert all(not t.any() for t in _sums(cal))
     cal.step(*batch)
     assert calls.cov[7:] == [1.0] * 5
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_all_calls_go_to_one_stream_of_the_weights_device(monkeypatch, given):
+    """Products, covariances and the quantizer's calls, whatever the process has
+    current."""
+    calls = Calls(kq(), monkeypatch)
+    cal, batch = _make()
+    dev = cal.Wg.device
+    side = _stream(dev, "side") if given else None
+    name = "side" if given else "current"
+    cal.step(*batch, stream=side)
+    assert len(calls.on) == 12
+    assert all(s != "process" and s.device == dev and s.name == name for s in calls.on)
+
+    class Engine:
+        H_X, H_G = torch.empty(128, 128), torch.empty(256, 256)
+
+        def run_from_covariances(self, W, stream=None):
+            assert calls.stack[-1] != "process" and calls.stack[-1].name == name
+            assert stream is None or stream is side
+            return W
+
+    assert cal.quantize("gate", Engine(), stream=side) is cal.Wg
+    assert calls.stack == ["process"]
+
+
+def test_stream_of_another_device_is_refused(monkeypatch):
+    calls = Calls(kq(), monkeypatch)
+    cal, batch = _make()
+    other = _stream(torch.device("cuda", 1))
+    for call in (lambda: cal.step(*batch, stream=other), lambda: cal.reset(stream=other),
+                 lambda: cal.quantize("gate", None, stream=other)):
+        with pytest.raises(ValueError):
+            call()
+    assert not calls.on

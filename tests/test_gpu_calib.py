@@ -255,3 +255,22 @@ def test_captured_before_anything_ran(cuda_device):
     both.replay()
     both.replay()
     same([b])
+
+
+def test_quantized_on_another_stream(cuda_device):
+    """The quantizer's calls and the copies around them keep to the stream given."""
+    kq()
+    from second_order_post_b200.calib import FeedForwardCalibration
+    from second_order_post_b200.engine import SublayerEngine
+    d, f, vocab, n = 256, 384, 520, 512
+    cal = FeedForwardCalibration(*_block(d, f, vocab, seed=20), max_tokens=n, tokens=n)
+    cal.step(*_batch(n, d, vocab, 8, 5))
+    want, got = (SublayerEngine(d, f, bits=4, rot_in=(128, 3), keep_w_rot=True) for _ in range(2))
+    cal.quantize("down", want)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    cal.quantize("down", got, stream=side)
+    side.synchronize()
+    got.check_info()
+    assert torch.equal(got.W_ref, want.W_ref) and torch.equal(got.W_rot, want.W_rot)
+    assert torch.equal(got.codes, want.codes)
