@@ -156,9 +156,9 @@ def kronq_accum_cov(A, H, alpha, beta, info, stream=None):
     """H = alpha * AᵀA + beta * H for A (n x d, bf16/fp32, row-major); info is
     a device int32 word (TIMEOUT when a pipeline wait ran out)."""
     n, d = A.shape
+    lda = A.stride(0) if n > 1 else d + 7 & -8   # (a single row's stride may be any)
     _check("kronq_accum_cov", _lib.kronq_accum_cov(
-        _stream(stream), _ptr(A), _dtype(A), n, d, A.stride(0), alpha, beta,
-        _ptr(H), _ptr(info)))
+        _stream(stream), _ptr(A), _dtype(A), n, d, lda, alpha, beta, _ptr(H), _ptr(info)))
 
 
 def kronq_sensitivity(H_X, H_G, out, stream=None):

@@ -274,3 +274,21 @@ def test_quantized_on_another_stream(cuda_device):
     got.check_info()
     assert torch.equal(got.W_ref, want.W_ref) and torch.equal(got.W_rot, want.W_rot)
     assert torch.equal(got.codes, want.codes)
+
+
+def test_one_token_of_any_stride(cuda_device):
+    kq()
+    from second_order_post_b200.calib import FeedForwardCalibration
+    d, f, vocab = 128, 256, 100
+    W = _block(d, f, vocab, seed=70)
+    X, *rest = _batch(1, d, vocab, 4, 1)
+    cals = [FeedForwardCalibration(*W, max_tokens=2, tokens=1) for _ in range(2)]
+    odd = X.reshape(-1).as_strided((1, d), (3, 1))
+    for cal, x in zip(cals, (X, odd)):
+        cal.step(x, *rest)
+    torch.cuda.synchronize()
+    for cal in cals:
+        cal.check_info()
+    for k in cals[0].H_X:
+        assert torch.equal(cals[0].H_X[k], cals[1].H_X[k])
+    assert float(cals[0].H_X["mlp"].trace()) > 0

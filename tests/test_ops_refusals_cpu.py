@@ -127,3 +127,16 @@ def test_binding_wants_cuda_tensors(K):
         K.kronq_gated(x, x, x, x, info)
     with pytest.raises(ValueError):
         K.kronq_distill_fwd(x, x, x, x, x, info)
+
+
+@pytest.mark.parametrize("rows,stride", [(1, 1), (1, 129), (1, 1000), (2, 136), (0, 128)])
+def test_covariance_of_a_single_row(K, monkeypatch, rows, stride):
+    """The stride of one row is not looked at, as in the products before it."""
+    import torch
+    got = []
+    monkeypatch.setattr(K._lib, "kronq_accum_cov", lambda *a: got.append(a[3:6]) or 0)
+    monkeypatch.setattr(K, "_stream", lambda s: None)
+    A = torch.zeros(1024, dtype=torch.bfloat16).as_strided((rows, 128), (stride, 1))
+    info = torch.zeros(1, dtype=torch.int32)
+    K.kronq_accum_cov(A, torch.zeros(128, 128), 1.0, 0.0, info)
+    assert got == [(rows, 128, stride if rows > 1 else 128)]
