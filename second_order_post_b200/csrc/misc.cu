@@ -80,6 +80,7 @@ namespace {
 std::atomic<int> g_last_cuda{0};
 }
 kronq_status cuda_fail(cudaError_t e) {
+  (void)cudaGetLastError();   // else the next call's launch check would report it again
   g_last_cuda.store(static_cast<int>(e), std::memory_order_relaxed);
   return KRONQ_ERR_CUDA;
 }

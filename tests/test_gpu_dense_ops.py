@@ -536,6 +536,47 @@ print("same")
     assert out.returncode == 0 and "same" in out.stdout, out.stderr[-2000:]
 
 
+def test_failed_launch_is_reported_once(cuda_device):
+    """A launch that fails (into a capture that another call has made invalid) fails
+    its own call, not the next one, which is in order."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from second_order_post_b200 import kronq as K
+X, W = torch.randn(8, 64, device="cuda").bfloat16(), torch.randn(32, 64, device="cuda").bfloat16()
+Y = torch.empty(8, 32, dtype=torch.bfloat16, device="cuda")
+A, H = torch.randn(16, 128, device="cuda"), torch.empty(128, 128, device="cuda")
+info = torch.zeros(1, dtype=torch.int32, device="cuda")
+K.kronq_linear(X, W, Y, info)
+torch.cuda.synchronize()
+want = Y.clone()
+side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+def fails(call):
+    try:
+        call()
+    except RuntimeError:
+        return True
+    return False
+with torch.cuda.stream(side):
+    graph.capture_begin()
+    assert fails(side.synchronize)
+    assert fails(lambda: K.kronq_linear(X, W, Y, info))
+    assert fails(graph.capture_end)
+K.kronq_accum_cov(A, H, 1.0, 0.0, info)
+K.kronq_linear(X, W, Y, info)
+torch.cuda.synchronize()
+assert info.item() == 0 and torch.equal(Y, want)
+assert float((H - A.T @ A).abs().max()) < 1e-3
+print("once")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert out.returncode == 0 and "once" in out.stdout, out.stderr[-2000:]
+
+
 def test_same_bits_twice(cuda_device):
     K = kq()
     n, d_in, d_out = 48, 2048, 640
