@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
   ts = block_reduce(ts, red, 0.f, add);
 
   // ---- log-sum-exp of the row
-  double lse;
+  double lse, log_s = 0.0;
   float m = -INFINITY, s = 0.f, shift = 0.f;
   if (FWD) {
     for (int64_t v = tid; v < a.vocab; v += DI_THREADS) m = max_nan(m, to_f(z[v]));
@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
     const Exponent ex(m, a.c);
     for (int64_t v = tid; v < a.vocab; v += DI_THREADS) s += ex.one(to_f(z[v]));
     s = block_reduce(s, red, 0.f, add);
-    lse = double(m) / double(a.tau) + log(double(s));
+    log_s = log(double(s));
+    lse = double(m) / double(a.tau) + log_s;
   } else {
     lse = a.lse[row];
     lse_reference(a.lse[row], a, m, shift);
@@ -169,7 +170,8 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
     const float p = i_s[j] >= 0 ? expf((t - tmax) / a.tau) / ts : 0.f;
     p_s[j] = p;
     if (FWD && p != 0.f)
-      loss += double(p) * ((double(t) - double(tmax) - double(z_s[j])) / double(a.tau) - lts + lse);
+      loss += double(p) * ((double(t) - double(tmax) + (double(m) - double(z_s[j]))) / double(a.tau) +
+                           (log_s - lts));
   }
   if (FWD) {
     loss = block_reduce(loss, red_d, 0.0, add);
@@ -329,19 +331,16 @@ __device__ __forceinline__ uint4 cut_vec(const T *z, int64_t e, int64_t vocab) {
 }
 
 // The loss and lse of a row from its (m, s), the teacher's sum and the warps' parts
-// of sum p (T - max T - z) and sum p (one thread).
+// of sum p (T - max T + m - z) (one thread). The differences come first: m itself may
+// be so large that even fp64 keeps nothing of them beside it.
 __device__ __forceinline__ void finish_loss(const DistillP &a, int64_t r, bool counts, float m,
-                                            float s, float ts, const double2 *parts_s, int np) {
+                                            float s, float ts, const double *parts_s, int np) {
   float l = 0.f, lse = 0.f;
   if (counts) {
-    double x = 0.0, y = 0.0;
-    for (int q = 0; q < np; ++q) {
-      x += parts_s[q].x;
-      y += parts_s[q].y;
-    }
+    double x = 0.0;
+    for (int q = 0; q < np; ++q) x += parts_s[q];
     const double ls = log_split(s);
-    l = float(double(a.tau) * double(a.tau) *
-              ((x + y * double(m)) * a.inv_tau + (ls - log_split(ts))));
+    l = float(double(a.tau) * double(a.tau) * (x * a.inv_tau + (ls - log_split(ts))));
     lse = float(double(m) * a.inv_tau + ls);
     if (!isfinite(l)) report(a.info, KRONQ_ERR_NONFINITE);
   }
@@ -362,7 +361,7 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
   int16_t *next_s = reinterpret_cast<int16_t *>(head_s + (2 << bits));   // [2][kp]
   __shared__ __align__(16) float4 wpair[32];         // (m, s) of the row, of the teacher
   __shared__ __align__(16) float4 pair[2];           // the CTA's (m, s)
-  __shared__ double2 loss_s[2][WARPS];
+  __shared__ double loss_s[2][WARPS];
   __shared__ uint64_t bar;
   __shared__ int abort_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -571,22 +570,19 @@ __global__ void __launch_bounds__(ST, wide_per_sm<ST>())
     // ---- the teacher's p (kept as w tau p) and its part of the loss
     if (counts && warp * 32 < k) {
       const float rts = __fdiv_rn(1.f, ts);
-      double x = 0.0, y = 0.0;
+      double x = 0.0;
       for (int j = tid; j < k; j += ST) {
         const float t = tr[j], zj = zr[j];
         const float p = ir[j] >= 0 ? ex2((t - tm) * c2e) * rts : 0.f;
-        if (FWD && rank == 0 && p != 0.f) {
-          x += double(p) * (double(t) - double(tm) - double(zj));
-          y += double(p);
-        }
+        if (FWD && rank == 0 && p != 0.f)
+          x += double(p) * (double(t) - double(tm) + (double(m) - double(zj)));
         tr[j] = wt * p;
         zr[j] = scale * ex.one(zj);
       }
       if (FWD && rank == 0) {
         __syncwarp();
         x = warp_sum_d(x);
-        y = warp_sum_d(y);
-        if (lane == 0) loss_s[par][warp] = make_double2(x, y);
+        if (lane == 0) loss_s[par][warp] = x;
       }
     }
     __syncthreads();
@@ -650,7 +646,7 @@ __global__ void __launch_bounds__(ST, 1024 / ST)
   __shared__ float t_s[DI_MAXK], z_s[DI_MAXK];
   __shared__ __align__(16) float4 wpair[WARPS];
   __shared__ __align__(16) float4 pair;
-  __shared__ double2 loss_s[WARPS];
+  __shared__ double loss_s[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % parts, k = a.k;
   const int64_t row = blockIdx.x / parts;
@@ -774,26 +770,20 @@ __global__ void __launch_bounds__(ST, 1024 / ST)
   // ---- the loss
   if (rank == 0) {
     const bool counts = tm != -INFINITY;   // some entry is kept
+    if (s == 0.f) m = NAN;   // no logit at all: q has no value
     const float rts = __fdiv_rn(1.f, ts);
-    double x0 = 0.0, y0 = 0.0;
+    double x0 = 0.0;
     if (counts) {
       for (int j = tid; j < k; j += ST) {
         const float t = t_s[j];
         const float p = t == -INFINITY ? 0.f : ex2((t - tm) * c2e) * rts;
-        if (p != 0.f) {
-          x0 += double(p) * (double(t) - double(tm) - double(z_s[j]));
-          y0 += double(p);
-        }
+        if (p != 0.f) x0 += double(p) * (double(t) - double(tm) + (double(m) - double(z_s[j])));
       }
     }
     x0 = warp_sum_d(x0);
-    y0 = warp_sum_d(y0);
-    if (lane == 0) loss_s[warp] = make_double2(x0, y0);
+    if (lane == 0) loss_s[warp] = x0;
     __syncthreads();
-    if (tid == 0) {
-      if (s == 0.f) m = NAN;   // no logit at all: q has no value
-      finish_loss(a, row, counts, m, s, ts, loss_s, kq_min(WARPS, (k + 31) / 32));
-    }
+    if (tid == 0) finish_loss(a, row, counts, m, s, ts, loss_s, kq_min(WARPS, (k + 31) / 32));
   }
   __syncwarp();
   // no CTA leaves while another may still read its pair
