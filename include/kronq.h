@@ -421,8 +421,8 @@ kronq_status kronq_dequant_matvec(kronq_stream_t stream, const kronq_opts *opts,
  *     whole pass. TIMEOUT when a pipeline wait ran out (the outputs are then
  *     not valid).
  *   - Outputs may not overlap inputs or one another, except where the call
- *     says so. No workspace is needed, and results do not depend on how the
- *     work was split: the same call gives the same bits.
+ *     says so. No workspace is needed, and the same call gives the same bits
+ *     (the order of its sums follows from the sizes and the device alone).
  *   - n = 0 (no tokens) is allowed: weight and bias gradients are then 0.
  * ---------------------------------------------------------------------------
  */
@@ -447,7 +447,8 @@ kronq_status kronq_linear(kronq_stream_t stream, const void *X, int64_t n,
  *   dX = dZ W + dXr          n x d_in bf16, or NULL; dXr: bf16 addend or NULL
  *                            (a residual stream's gradient; may be dX itself)
  *   dW = dZ^T X              d_out x d_in bf16, or NULL
- * The products take dZ as rounded to bf16. With KRONQ_ACT_NONE dZ = dY: Z is
+ * The products take dZ as rounded to bf16 (the tensor cores' operand type),
+ * db is an fp32 sum. With KRONQ_ACT_NONE dZ = dY: Z is
  * not read, and dZ may be NULL or dY (otherwise it receives a copy). dZ may
  * also be dY or Z with another activation (the same stride). X may be NULL
  * without dW, W without dX.
@@ -481,7 +482,7 @@ kronq_status kronq_gated(kronq_stream_t stream, const void *X, int64_t n,
  *   dX = Gg Wg + Gu Wu + dXr  n x d bf16, or NULL; dXr: bf16 addend or NULL
  *                           (may be dX itself)
  *   dWg = Gg^T X, dWu = Gu^T X  f x d bf16 with stride lddw, both or neither
- * The products take Gg and Gu as rounded to bf16. Gg or Gu may be A, U or dH
+ * The products take Gg and Gu as rounded to bf16, as above. Gg or Gu may be A, U or dH
  * (the same stride; not both the same matrix). X may be NULL without the
  * weight gradients, Wg and Wu without dX.
  */

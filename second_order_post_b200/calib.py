@@ -17,6 +17,10 @@ tokens, and enqueues on one CUDA stream, per batch:
   sums      H_X of gate/up (X) and of down (H), H_G of gate (Gg), up (Gu) and
             down (dY)                            kronq_accum_cov
 
+The block is the model's last: its output goes to the head as it is, without a
+norm. A gradient that comes from a later block, or a norm between, takes the same
+library calls by hand.
+
 The weights are not updated: no weight gradient is formed. All arithmetic runs
 in the library's kernels; this module allocates, passes pointers and keeps the
 status words of all batches together.
@@ -89,9 +93,11 @@ class FeedForwardCalibration:
 
     def step(self, X, T, idx, weight=None, stream=None):
         """Adds one batch to the sums: X (n x d bf16 tokens), the teacher's top logits T and
-        their places idx (n x k), weight (n fp32, None: all 1). Returns the
-        tokens' losses and dX, the gradient with respect to X (views that the
-        next step overwrites)."""
+        their places idx (n x k), weight (n fp32, None: all 1) of a token's loss.
+        Every row of X is a token of H_X, one of weight 0 too, and has to be
+        finite: padding is left out of the batch. Returns the tokens' losses and dX,
+        the gradient with respect to X (views that the next step overwrites). A step
+        that raises may have added a part of its batch: reset()."""
         n = X.shape[0]
         if not 1 <= n <= self.max_tokens:
             raise ValueError(f"a batch has 1 to {self.max_tokens} tokens, not {n}")

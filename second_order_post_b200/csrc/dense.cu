@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const ActBwdP p) {
 // a thread sums 8 columns of its rows, and the threads and then the CTAs meet
 // in a fixed order (the first CTA reads the others' sums through distributed
 // shared memory). Bound by reading dY and Z and writing dZ once: 4096 x 4096 with
-// relu take 19.5 us (5.2 TB/s), with gelu 31.4 us, bound by its instructions; a wave
+// relu take 19.5 us (5.2 TB/s), with gelu 31.1 us, bound by its instructions; a wave
 // and a half of CTAs costs more than fewer parts (2048 x 11008 25.2 us in three parts,
 // 31.5 in eight).
 constexpr int BG_MAXC = 8;
@@ -1231,6 +1231,11 @@ kronq_status gated_fwd(cudaStream_t st, int64_t n, int64_t d, int64_t f, const M
   return tokens_product<true, false>(st, Operands{X, Wg, Mat{}, Wu}, p, act);
 }
 
+// The products take dZ (below: Gg and Gu) as stored, rounded to bf16: that is the
+// operand type of the tensor cores, and the sublayer's G that the caller gets. An fp32
+// dZ would be a sum of two or three bf16 parts and as many products. It costs a second
+// rounding: 4096 tokens of 4096 x 4096 are 2.3e-3 from the fp64 definition (norm of
+// the error over the norm) where one rounding of the result alone is 1.7e-3.
 kronq_status linear_bwd(cudaStream_t st, int64_t n, int64_t d_in, int64_t d_out, const Mat &dY,
                         const Mat &Z, int act, const Mat &X, const Mat &W, const Mat &dZ,
                         float *db, const Mat &dXr, const Mat &dX, const Mat &dW, int32_t *info) {

@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(DI_THREADS) distill_kernel(const DistillP a) {
     const float p = i_s[j] >= 0 ? expf((t - tmax) / a.tau) / ts : 0.f;
     p_s[j] = p;
     if (FWD && p != 0.f)
-      loss += double(p) * ((double(t) - double(tmax) + (double(m) - double(z_s[j]))) / double(a.tau) +
-                           (log_s - lts));
+      loss += double(p) * ((double(t) - double(tmax) + (double(m) - double(z_s[j]))) /
+                               double(a.tau) + (log_s - lts));
   }
   if (FWD) {
     loss = block_reduce(loss, red_d, 0.0, add);
@@ -266,16 +266,16 @@ __device__ __forceinline__ void warp_pair(float &m, float &s, float c) {
 //   An entry needs the sum over all entries that name its place: they are found
 // in a list of those whose places share a hash (about one entry long, made while
 // the row is on its way) and added in the order of their numbers. (Comparing with
-// all k entries cost 314 us for 1024 rows of 32000 bf16 logits and k = 1024, 60 us
+// all k entries cost 314 us for 1024 rows of 32000 bf16 logits and k = 1024, 63 us
 // with the lists, backward alone; the same 27 us at k = 64.)
 //   The copy takes whole 16-byte vectors inside the row; the threads that own
 // the row's first and last vector put those together when they are cut.
 //   Sizes: 384 threads and three CTAs an SM, or for rows of up to 22 KB 128
 // threads and up to nine, of up to 6 KB 64 threads and up to sixteen.
-// Measured (4096 rows of 32000 bf16 logits, k = 64, with the gradient): three
-// CTAs of 384 threads 107 us, two of 512 threads 120 us, six of 192 threads on
-// half rows (clusters of two) 121 us; the row in registers, one CTA of 512
-// threads an SM, 135 us (its phases do not overlap).
+// Measured (4096 rows of 32000 bf16 logits, k = 64, with the gradient; 110 us as it
+// is): three CTAs of 384 threads 107 us, two of 512 threads 120 us, six of 192
+// threads on half rows (clusters of two) 121 us; the row in registers, one CTA of
+// 512 threads an SM, 135 us (its phases do not overlap).
 constexpr int WIDE_VEC = 4400;   // vectors of a part at most: 70 KB
 template <int ST>
 constexpr int wide_per_sm() {
