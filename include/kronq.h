@@ -508,9 +508,10 @@ kronq_status kronq_gated_bwd(kronq_stream_t stream, const void *dH,
  * so dZ is the gradient of sum over rows of weight * loss. A place may be
  * named more than once: its p's add up. weight: n fp32, or NULL for all 1. A
  * row of weight 0, or one that keeps no entry, does not count: its logits do
- * not matter (they may be NaN), and its loss, lse and gradient are 0. Row sums are fp32, the
- * row's logarithms and its loss fp64, rounded once. info_dev: NONFINITE when
- * the loss of a row that counts is not finite.
+ * not matter (they may be NaN), and its loss, lse and gradient are 0. Row sums
+ * of exponentials are fp32, their logarithms good to 4e-8 and added up with the
+ * loss in fp64, which is rounded once; the error of lse enters the loss times
+ * tau^2. info_dev: NONFINITE when the loss of a row that counts is not finite.
  * _fwd writes loss and lse (n fp32), _bwd takes that lse and writes dZ (n x
  * vocab, zdtype), _step does both while a row is on the chip. _bwd's q_v is
  * exp(Z_v / tau - lse) for the lse it is given, which fp32 holds to 2^-24 of
