@@ -87,10 +87,13 @@ __device__ __forceinline__ void act_df(float z, float &h, float &dh) {
     // beyond |z| = 30 the derivative's second term is 0 in fp32; the clamp
     // keeps its polynomial finite there
     const float zc = fminf(fmaxf(z, -30.f), 30.f);
-    const float s = logistic(1.5957691216f * fmaf(0.044715f * zc * zc, z, z));
+    const float e = __expf(-1.5957691216f * fmaf(0.044715f * zc * zc, z, z));
+    const float s = __fdividef(1.f, 1.f + e);
+    // 1 - s is e s: the difference drops up to 2^-23, and z dv2 is 36 at z = 5
+    const float r = e < 1.f ? e * s : 1.f - s;
     const float dv2 = 1.5957691216f * fmaf(3.f * 0.044715f * zc, zc, 1.f);
     h = z * s;
-    dh = fmaf(h * (1.f - s), dv2, s);
+    dh = fmaf(h * r, dv2, s);
   } else {
     h = z;
     dh = 1.f;

@@ -647,3 +647,22 @@ def test_activation_at_every_bf16_value(act):
     y, dy = act64(X.double(), act)
     close(Y, y, (EVAL + HALF_BF16) * y.abs() + 1e-30)
     close(dZ, dy, EVAL * LIP + HALF_BF16 * dy.abs())
+
+
+@pytest.mark.parametrize("act", [a for a in ACTS if a != "none"])
+def test_derivative_in_fp32_at_every_bf16_value(act):
+    """The same through db, which is not rounded to bf16: with one token and dY = 1 it
+    is act'(z), to 2^-20 of the derivative's largest value."""
+    k = kq()
+    bits = torch.arange((127 - 20) << 7, (127 + 6) << 7, dtype=torch.int32)
+    pos = bits.to(torch.int16).view(torch.bfloat16)
+    Z = torch.cat([pos, -pos]).view(1, -1).cuda()
+    w = Z.shape[1]
+    info = torch.zeros(1, dtype=torch.int32, device="cuda")
+    X, dZ = torch.zeros(1, 8, dtype=torch.bfloat16, device="cuda"), torch.empty_like(Z)
+    db = torch.empty(w, device="cuda")
+    k.kronq_linear_bwd(torch.ones_like(Z), X, None, info, act=k.KRONQ_ACTS[act], Z=Z, dZ=dZ, db=db)
+    torch.cuda.synchronize()
+    assert info.item() == 0
+    dy = act64(Z.double()[0], act)[1]
+    close(db, dy, EVAL * LIP + 0 * dy)
