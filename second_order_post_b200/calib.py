@@ -146,7 +146,9 @@ class FeedForwardCalibration:
             return engine.run_from_covariances(self.weight(sublayer))
 
     def check_info(self):
-        """Raises KronqError for a status word that is not 0 (syncs)."""
+        """Raises KronqError for a status word that is not 0, once all that is enqueued
+        on the weights' device, on whichever stream, has run."""
+        torch.cuda.synchronize(self.Wg.device)
         v = int(self.info.item())
         if v:
             raise K.KronqError("kronq calibration pass", v & 0xFF)

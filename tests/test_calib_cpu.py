@@ -24,6 +24,8 @@ class Calls:
         self.stack = ["process"]
         monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: _stream(dev))
         monkeypatch.setattr(torch.cuda, "stream", self.current)
+        self.synced = []
+        monkeypatch.setattr(torch.cuda, "synchronize", self.synced.append)
 
     @contextlib.contextmanager
     def current(self, stream):
@@ -158,3 +160,12 @@ def test_stream_of_another_device_is_refused(monkeypatch):
         with pytest.raises(ValueError):
             call()
     assert not calls.on
+
+
+def test_status_is_read_behind_every_stream(monkeypatch):
+    """The pass may have gone to another stream than the reader's."""
+    calls = Calls(kq(), monkeypatch)
+    cal, batch = _make()
+    cal.step(*batch, stream=_stream(cal.Wg.device, "side"))
+    cal.check_info()
+    assert calls.synced == [cal.Wg.device]

@@ -292,3 +292,24 @@ def test_one_token_of_any_stride(cuda_device):
     for k in cals[0].H_X:
         assert torch.equal(cals[0].H_X[k], cals[1].H_X[k])
     assert float(cals[0].H_X["mlp"].trace()) > 0
+
+
+def test_status_of_a_pass_still_under_way(cuda_device):
+    """check_info right behind a step on another stream that has not started yet."""
+    K = kq()
+    from second_order_post_b200.calib import FeedForwardCalibration
+    d, f, vocab, n = 128, 128, 100, 16
+    cal = FeedForwardCalibration(*_block(d, f, vocab, seed=60), max_tokens=n, tokens=n)
+    batch = _batch(n, d, vocab, 4, 3)
+    side = torch.cuda.Stream()
+    cal.step(*batch, stream=side)         # kernels are loaded
+    cal.check_info()
+    batch[0][2, 7] = float("nan")
+    batch[3][2] = 1.0
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(int(1e8))       # some 50 ms
+    cal.step(*batch, stream=side)
+    with pytest.raises(K.KronqError) as err:
+        cal.check_info()
+    assert err.value.status == K.KRONQ_ERR_NONFINITE
